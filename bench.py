@@ -169,11 +169,12 @@ def measured_hbm_peak():
 
 
 def decode_source_hash() -> str:
-    """Hash of the decode kernel's code (decode.cu, device_utils.cuh and
-    order.cuh with comments and blank space removed, so a comment edit
+    """Hash of the decode kernel's code (decode.cu, decode_common.cuh,
+    device_utils.cuh and order.cuh with comments and blank space removed, so a comment edit
     keeps a capture current and any code change makes it stale)."""
     h = hashlib.sha256()
-    for name in ("decode.cu", "device_utils.cuh", "order.cuh"):
+    for name in ("decode.cu", "decode_common.cuh", "device_utils.cuh",
+                 "order.cuh"):
         with open(os.path.join(ROOT, "paged_kv_cache_383_b200", "csrc",
                                name)) as f:
             text = f.read()
