@@ -32,7 +32,8 @@
  *     pa_decode ([KV-cache chapter] "PagedAttention: borrowing virtual
  *     memory...": a private copy is made before the first write into a shared
  *     block).
- *   - pa_cache_write, pa_copy_blocks, pa_decode and pa_prefill only enqueue
+ *   - pa_cache_write, pa_append, pa_copy_blocks, pa_decode and pa_prefill
+ *     (and their _q8 forms) only enqueue
  *     kernels (no allocation, no synchronisation), so a sequence of them
  *     can be captured in a CUDA graph and replayed; the graph keeps the
  *     pointers and shapes it was captured with.  Call each shape once
@@ -378,6 +379,179 @@ pa_status pa_swap_blocks(void* dst_k_cache, void* dst_v_cache,
                          int num_kv_heads, int head_dim, int block_size,
                          int num_src_blocks, int num_dst_blocks,
                          pa_dtype dtype, int32_t* dev_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Append new tokens: norm and position rotation of their queries and keys,
+ * and the write of their keys and values, in one launch.  (No counterpart in
+ * the pages: they store a new token's K and V as given; this is what stands
+ * between a layer's projections and its attention in the models served.)
+ *
+ * Row t of q, k and v belongs to sequence b with query_start[b] <= t <
+ * query_start[b+1] and is its new token i = t - query_start[b], at position
+ * p = L - q_len + i with L = context_lens[b] (the new tokens included) and
+ * q_len = query_start[b+1] - query_start[b]: the convention of pa_prefill,
+ * whose query_start, block_tables and context_lens serve here too.  With
+ * query_start NULL each sequence has one new token, row t being sequence t's
+ * (a decode step; total_q = num_seqs).  For each query and key head x:
+ *   norm      x <- w x / sqrt(mean(x^2) + norm_eps), w = q_norm or k_norm
+ *             [head_dim] of dtype; NULL: none
+ *   rotation  pair j of the first rot_dim elements turns by p rope_freqs[j]:
+ *             (u, w) <- rope_scale (u cos - w sin, w cos + u sin); pair j is
+ *             (j, j + rot_dim / 2) (PA_ROPE_HALF) or (2j, 2j + 1)
+ *             (PA_ROPE_INTERLEAVED).  rot_dim 0: none
+ * then q_out[t] = the queries, and the key and value heads go to slot
+ * p % block_size of block block_tables[b][p / block_size].  Computed in fp32
+ * (angles in fp64) and rounded once; pa_append copies V exactly.
+ * Layouts: q [total_q, num_q_heads, head_dim], k, v [total_q, num_kv_heads,
+ * head_dim], q_out like q: the heads of a row dense, rows q_stride, k_stride,
+ * v_stride, q_out_stride elements apart (multiples of 8, at least a row), so
+ * slices of one projection's output need no copy.  q_out may be q itself
+ * (same stride); otherwise no output may overlap an input.  num_q_heads 0:
+ * keys and values only (q, q_out ignored).  rope_freqs: device float64
+ * [rot_dim / 2], e.g. from pa_rope_freqs.  The caches as for pa_decode.
+ * Supported: head_dim 64 or 128, block_size 16 or 32, rot_dim a multiple of
+ * 16 up to head_dim.
+ * A sequence with context length 0 is padding: its rows are neither read nor
+ * written.  Rows behind the last sequence, and every cache slot but the new
+ * tokens', stay as they are.
+ * Two sequences must not append to one physical block in one call (copy
+ * shared blocks first).  Device-side: a context or query range outside the
+ * table or the rows, or more new tokens than max_q_len, sets *dev_err =
+ * PA_ERR_DEVICE_OOB and the sequence's rows are not written; a block id
+ * outside the pool sets it and that token's K and V are not written.
+ * Only enqueues one kernel (launched programmatically: it waits for the
+ * kernel before it), so it can be captured; no workspace.
+ * ---------------------------------------------------------------------- */
+typedef enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+
+typedef struct {
+  int num_seqs;
+  int num_q_heads;       /* 0: keys and values only */
+  int num_kv_heads;
+  int head_dim;
+  int block_size;
+  int max_blocks_per_seq;
+  int num_blocks;
+  pa_dtype dtype;        /* of q, k, v, the norm weights and q_out */
+  int total_q;           /* rows of q, k, v and q_out */
+  int max_q_len;         /* host bound on any sequence's new tokens */
+  int rot_dim;           /* leading elements of a head that turn; 0: none */
+  int rope_layout;       /* pa_rope_layout */
+  float rope_scale;      /* factor of cos and sin (usually 1) */
+  float norm_eps;
+  int64_t q_stride;      /* elements between rows */
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t q_out_stride;
+} pa_append_desc;
+
+pa_status pa_append(void* q_out, void* k_cache, void* v_cache, const void* q,
+                    const void* k, const void* v, const void* q_norm,
+                    const void* k_norm, const double* rope_freqs,
+                    const int32_t* block_tables, const int32_t* context_lens,
+                    const int32_t* query_start, const pa_append_desc* desc,
+                    int32_t* dev_err, void* stream);
+
+/* Angular frequencies (radians per position) of the rot_dim / 2 pairs, into
+ * host freqs_out, and the factor for rope_scale into *scale_out.  Host only.
+ *   PA_ROPE_PLAIN       f_j = base^(-2j / rot_dim)
+ *   PA_ROPE_LINEAR      f_j / factor
+ *   PA_ROPE_WAVELENGTH  by the turns r = original_len f_j / 2 pi a pair makes
+ *                       over the trained length: f_j / factor for r <= low,
+ *                       f_j for r >= high, linear in r between
+ *   PA_ROPE_YARN        the same mix, linear in the pair's index between the
+ *                       pairs that turn high and low times (rounded
+ *                       outwards), and *scale_out = 0.1 ln(factor) + 1
+ * *scale_out is 1 elsewhere. */
+typedef enum {
+  PA_ROPE_PLAIN = 0,
+  PA_ROPE_LINEAR = 1,
+  PA_ROPE_WAVELENGTH = 2,
+  PA_ROPE_YARN = 3
+} pa_rope_scaling;
+
+typedef struct {
+  int rot_dim;
+  int scaling;        /* pa_rope_scaling */
+  int original_len;   /* trained context length (WAVELENGTH, YARN) */
+  double base;        /* > 1 */
+  double factor;      /* >= 1 (all but PLAIN) */
+  double low, high;   /* turns, 0 < low < high (WAVELENGTH, YARN) */
+} pa_rope_desc;
+
+pa_status pa_rope_freqs(const pa_rope_desc* desc, double* freqs_out,
+                        float* scale_out);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit cache.  (No counterpart in the pages.)
+ *   k_cache, v_cache    [num_blocks, num_kv_heads, block_size, head_dim] of
+ *                       8-bit floats e4m3 (4 exponent bits, 3 fraction bits,
+ *                       largest 448, no infinities), 16-byte aligned
+ *   k_scales, v_scales  [num_blocks, num_kv_heads] float32, positive
+ * hold, for each block and KV head, the values code * scale: half the bytes
+ * of a 16-bit cache (plus 8 bytes a block and head).  The block manager, the
+ * tables and the lengths are those of the 16-bit cache.  A float format
+ * keeps its relative precision (2^-4) over 15 binades, so the scales that
+ * pa_append_q8 chooses are powers of two: nothing is lost against others,
+ * and codes that follow a grown scale move exactly unless they become
+ * subnormal.  Attention accepts any positive finite scales (2^-100 to 2^100;
+ * a scale of 0 stands for a block of zeros).
+ *
+ * pa_append_q8 -- pa_append into this cache.  For a block and head of which
+ * the call writes slots o .. o + m - 1 (always a run), with A the largest
+ * magnitude among the m new rows (K after norm and rotation, in fp32) and N
+ * the smallest power of two in [2^-64, 2^120] with A <= 448 N:
+ *     scale' = o > 0 ? max(scale, N) : N
+ *     code   = e4m3(x / scale')    new rows; nearest even, infinities become
+ *                                  +-448 and NaN stays NaN
+ *     code   = e4m3(code * scale / scale')   slots 0 .. o - 1, if it grew
+ * Slot 0 starts a block anew: its former codes and scale do not count.
+ * Deterministic: the result does not depend on the order of the rows.
+ * (A prompt appended in one call and in pieces may differ: a piece's codes
+ * are rounded before later tokens are known.) */
+pa_status pa_append_q8(void* q_out, void* k_cache, void* v_cache,
+                       float* k_scales, float* v_scales, const void* q,
+                       const void* k, const void* v, const void* q_norm,
+                       const void* k_norm, const double* rope_freqs,
+                       const int32_t* block_tables,
+                       const int32_t* context_lens,
+                       const int32_t* query_start, const pa_append_desc* desc,
+                       int32_t* dev_err, void* stream);
+
+/* pa_decode over the 8-bit cache: the same descriptor (dtype is that of q
+ * and out; kernel PA_KERNEL_SIMT is PA_ERR_UNSUPPORTED), workspace
+ * (pa_decode_workspace_bytes), launches, checks and errors.  Products of q
+ * and the weights with the codes run on the tensor cores in fp16 (the codes
+ * are exact there), scales and softmax in fp32. */
+pa_status pa_decode_q8(void* out, const void* q, const void* k_cache,
+                       const void* v_cache, const float* k_scales,
+                       const float* v_scales, const int32_t* block_tables,
+                       const int32_t* context_lens, float scale,
+                       const pa_decode_desc* desc, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_err,
+                       void* stream);
+
+/* pa_copy_blocks and pa_swap_blocks for the 8-bit cache: codes and scales of
+ * whole blocks.  Pairs, pools and errors as there; head_dim a multiple of
+ * 16. */
+pa_status pa_copy_blocks_q8(void* k_cache, void* v_cache, float* k_scales,
+                            float* v_scales, const int32_t* pairs,
+                            int num_pairs, int num_kv_heads, int head_dim,
+                            int block_size, int num_blocks, int32_t* dev_err,
+                            void* stream);
+pa_status pa_swap_blocks_q8(void* dst_k_cache, void* dst_v_cache,
+                            float* dst_k_scales, float* dst_v_scales,
+                            const void* src_k_cache, const void* src_v_cache,
+                            const float* src_k_scales,
+                            const float* src_v_scales, const int32_t* pairs,
+                            int num_pairs, int num_kv_heads, int head_dim,
+                            int block_size, int num_src_blocks,
+                            int num_dst_blocks, int32_t* dev_err,
+                            void* stream);
+
+/* pa_pool_blocks for the 8-bit cache (codes and scales of every layer). */
+int64_t pa_pool_blocks_q8(uint64_t bytes, int num_layers, int num_kv_heads,
+                          int head_dim, int block_size);
 
 /* ------------------------------------------------------------------------
  * Host block manager: free block pool, per-sequence logical->physical block

@@ -23,6 +23,8 @@ Modules.
   K/V (the plain definition the pages say paging leaves unchanged).
 * ``fragmentation``  -- block counts, waste and sharing arithmetic of the
   worked examples.
+* ``append``         -- norm, rotation, paged write and 8-bit quantisation of
+  appended tokens.
 * ``block_model``    -- a reference model of the block manager's semantics
   (free pool, on-demand allocation, reference counts, fork, copy-on-write),
   kept as plain Python lists and dicts.

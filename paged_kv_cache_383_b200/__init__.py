@@ -16,6 +16,9 @@ Layouts (see include/pagedkv.h for the full contract):
   k, v (new tokens) [num_tokens, num_kv_heads, head_dim]
   slot_mapping      [num_tokens] int64
   pairs             [num_pairs, 2] int32
+8-bit cache (the ``*_q8`` calls):
+  k_cache, v_cache  as above, torch.float8_e4m3fn
+  k_scales, v_scales  [num_blocks, num_kv_heads] float32
 """
 from __future__ import annotations
 
@@ -30,6 +33,9 @@ __all__ = [
     "pa_decode", "pa_decode_noalloc", "pa_prefill", "pa_prefill_workspace_bytes",
     "pa_cache_write",
     "pa_copy_blocks",
+    "pa_append", "pa_append_q8", "pa_rope_freqs", "pa_decode_q8",
+    "pa_copy_blocks_q8", "pa_swap_blocks_q8",
+    "pa_pool_blocks_q8",
     "pa_decode_workspace_bytes", "pa_decode_partition_size", "make_desc",
     "BlockManager", "PagedKVError", "NoFreeBlocksError", "library_path",
     "pa_launch_count", "pa_read_probe", "pa_wait_probe",
@@ -380,6 +386,303 @@ def pa_copy_blocks(k_cache, v_cache, pairs, *, dev_err=None, stream=None):
         head_dim, block_size, num_blocks, _dtype_code(k_cache),
         _dev(dev_err, "dev_err", torch.int32), _stream(stream))
     _lib.check(st, "pa_copy_blocks")
+
+
+# -- rotating append, 8-bit cache ---------------------------------------------
+_ROPE_LAYOUTS = {"half": _lib.PA_ROPE_HALF,
+                 "interleaved": _lib.PA_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {None: _lib.PA_ROPE_PLAIN, "linear": _lib.PA_ROPE_LINEAR,
+                  "wavelength": _lib.PA_ROPE_WAVELENGTH,
+                  "yarn": _lib.PA_ROPE_YARN}
+
+
+def _on_current(*named):
+    """Pointers of contiguous tensors that live on the current device
+    (``(tensor, name, dtype or None)`` each; None tensors give NULL).  The
+    library launches there: a tensor of another device is refused."""
+    import torch
+    dev = torch.cuda.current_device()
+    out = []
+    for t, name, dtype in named:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current "
+                             f"device (cuda:{dev}), is on {t.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _workspace(need: int, device, stream):
+    """A workspace of the call's own.  torch hands its memory out again on
+    the stream it was allocated on, so one used on another stream is marked
+    as in use there."""
+    import torch
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        s = torch.cuda.ExternalStream(stream, device=device) \
+            if isinstance(stream, int) else stream
+        if s != torch.cuda.current_stream():
+            ws.record_stream(s)
+    return ws
+
+
+def _check_q8(k_cache, v_cache, k_scales, v_scales, names=("", "")):
+    """Shapes of an 8-bit pool; returns (num_blocks, heads, block, dim)."""
+    a, b = names
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"{a}k_cache and {a}v_cache must be [num_blocks, "
+                         "num_kv_heads, block_size, head_dim]")
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+        raise ValueError(f"{a}k_scales and {a}v_scales must be [num_blocks, "
+                         "num_kv_heads]")
+    return shape
+
+
+def pa_rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling=None,
+                  factor: float = 1.0, original_len: int = 0,
+                  low: float = 1.0, high: float = 4.0):
+    """(freqs, rope_scale) for ``pa_append``: the angular frequencies of the
+    rot_dim/2 pairs as a float64 CPU tensor (move it to the device once) and
+    the factor of cos and sin.  ``scaling``: None, "linear", "wavelength" or
+    "yarn" (``low`` / ``high``: turns over ``original_len``)."""
+    import torch
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r} is none of "
+                         f"{list(_ROPE_SCALINGS)}")
+    d = _lib.pa_rope_desc(rot_dim=rot_dim, scaling=_ROPE_SCALINGS[scaling],
+                          original_len=original_len, base=base, factor=factor,
+                          low=low, high=high)
+    out = (ctypes.c_double * max(rot_dim // 2, 1))()
+    sc = ctypes.c_float()
+    _lib.check(_lib.load().pa_rope_freqs(ctypes.byref(d), out,
+                                         ctypes.byref(sc)), "pa_rope_freqs")
+    return torch.tensor(list(out), dtype=torch.float64), float(sc.value)
+
+
+def _rows(t, name: str, heads: int, head_dim: int, total: int, dt):
+    """Row stride of a [total, heads, head_dim] tensor whose heads are dense
+    within a row (a slice of a projection's output, say)."""
+    if t.shape != (total, heads, head_dim):
+        raise ValueError(f"{name} must be [{total}, {heads}, {head_dim}], is "
+                         f"{list(t.shape)}")
+    if t.dtype != dt:
+        raise TypeError(f"{name} dtype {t.dtype} != {dt}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and head_dim > 1) or (s1 != head_dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be dense "
+                         f"(strides {t.stride()})")
+    return s0 if total > 1 else heads * head_dim
+
+
+def _append(fn, name, q_out, k_cache, v_cache, scales, q, k, v, block_tables,
+            context_lens, query_start, max_q_len, q_norm, k_norm, norm_eps,
+            rope_freqs, rope_layout, rope_scale, dev_err, stream):
+    import torch
+    num_blocks, hkv, block_size, head_dim = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    total, dt = k.shape[0], k.dtype
+    num_seqs = context_lens.shape[0]
+    if context_lens.dim() != 1 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != num_seqs:
+        raise ValueError("context_lens must be [num_seqs] and block_tables "
+                         "[num_seqs, max_blocks_per_seq]")
+    if query_start is None:
+        if total != num_seqs:
+            raise ValueError("without query_start there is one row per "
+                             f"sequence: {num_seqs} sequences, {total} rows")
+        max_q_len = 1
+    else:
+        if query_start.shape != (num_seqs + 1,):
+            raise ValueError("query_start must be [num_seqs + 1]")
+        if max_q_len is None:
+            max_q_len = total
+    if rope_layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"rope_layout {rope_layout!r} is none of "
+                         f"{list(_ROPE_LAYOUTS)}")
+    ks = _rows(k, "k", hkv, head_dim, total, dt)
+    vs = _rows(v, "v", hkv, head_dim, total, dt)
+    hq = qs = os = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        hq = q.shape[1]
+        qs = _rows(q, "q", hq, head_dim, total, dt)
+        os = _rows(q_out, "q_out", hq, head_dim, total, dt)
+    for w, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None and w.shape != (head_dim,):
+            raise ValueError(f"{n} must be [{head_dim}]")
+    rot_dim = 0
+    if rope_freqs is not None:
+        if rope_freqs.dim() != 1:
+            raise ValueError("rope_freqs must be [rot_dim / 2]")
+        rot_dim = 2 * rope_freqs.shape[0]
+    desc = _lib.pa_append_desc(
+        num_seqs, hq, hkv, head_dim, block_size, block_tables.shape[1],
+        num_blocks, _dtype_code(k), total, max_q_len, rot_dim,
+        _ROPE_LAYOUTS[rope_layout], rope_scale, norm_eps, qs, ks, vs, os)
+    cache_dt = torch.float8_e4m3fn if scales else dt
+    ptrs = _on_current(
+        (k_cache, "k_cache", cache_dt), (v_cache, "v_cache", cache_dt),
+        *scales, (q_norm, "q_norm", dt), (k_norm, "k_norm", dt),
+        (rope_freqs, "rope_freqs", torch.float64),
+        (block_tables, "block_tables", torch.int32),
+        (context_lens, "context_lens", torch.int32),
+        (query_start, "query_start", torch.int32),
+        (dev_err, "dev_err", torch.int32))
+    dev = k_cache.get_device()
+    rows = []
+    for t, n in ((q_out, "q_out"), (q, "q"), (k, "k"), (v, "v")):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{n} is on {t.device}, not cuda:{dev}")
+        rows.append(None if t is None else t.data_ptr())
+    n = 2 + len(scales)
+    st = fn(rows[0], *ptrs[:n], *rows[1:], *ptrs[n:-1], ctypes.byref(desc),
+            ptrs[-1], _stream(stream))
+    _lib.check(st, name)
+    return q_out
+
+
+def pa_append(q_out, k_cache, v_cache, q, k, v, block_tables, context_lens,
+              query_start=None, *, max_q_len: int | None = None, q_norm=None,
+              k_norm=None, norm_eps: float = 1e-6, rope_freqs=None,
+              rope_layout: str = "half", rope_scale: float = 1.0,
+              dev_err=None, stream=None):
+    """Norm (``q_norm`` / ``k_norm``: [head_dim] weights) and position
+    rotation (``rope_freqs``: float64 [rot_dim/2], see ``pa_rope_freqs``) of
+    the new tokens' queries and keys, queries into ``q_out``, keys and values
+    into the paged cache, in one launch.  Rows as for ``pa_prefill``: the
+    last tokens of each context; without ``query_start`` one row per
+    sequence (a decode step).  q, k, v and q_out may be row slices of a wider
+    tensor; q_out may be q.  Returns ``q_out``."""
+    return _append(_lib.load().pa_append, "pa_append", q_out, k_cache,
+                   v_cache, (), q, k, v, block_tables, context_lens,
+                   query_start, max_q_len, q_norm, k_norm, norm_eps,
+                   rope_freqs, rope_layout, rope_scale, dev_err, stream)
+
+
+def pa_append_q8(q_out, k_cache, v_cache, k_scales, v_scales, q, k, v,
+                 block_tables, context_lens, query_start=None, *,
+                 max_q_len: int | None = None, q_norm=None, k_norm=None,
+                 norm_eps: float = 1e-6, rope_freqs=None,
+                 rope_layout: str = "half", rope_scale: float = 1.0,
+                 dev_err=None, stream=None):
+    """``pa_append`` into the 8-bit cache: e4m3 codes and one power-of-two
+    scale per (block, KV head), older codes of a block following a scale
+    that grows.  Returns ``q_out``."""
+    import torch
+    _check_q8(k_cache, v_cache, k_scales, v_scales)
+    return _append(_lib.load().pa_append_q8, "pa_append_q8", q_out, k_cache,
+                   v_cache, ((k_scales, "k_scales", torch.float32),
+                             (v_scales, "v_scales", torch.float32)),
+                   q, k, v, block_tables, context_lens, query_start,
+                   max_q_len, q_norm, k_norm, norm_eps, rope_freqs,
+                   rope_layout, rope_scale, dev_err, stream)
+
+
+def _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
+                    block_tables, context_lens, workspace, dev_err):
+    import torch
+    _check_q8(k_cache, v_cache, k_scales, v_scales)
+    if out.shape != q.shape:
+        raise ValueError("q and out disagree on shape")
+    if context_lens.shape != block_tables.shape[:1]:
+        raise ValueError("context_lens must be [num_seqs]")
+    e4m3, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    return _on_current(
+        (out, "out", None), (q, "q", None), (k_cache, "k_cache", e4m3),
+        (v_cache, "v_cache", e4m3), (k_scales, "k_scales", f32),
+        (v_scales, "v_scales", f32), (block_tables, "block_tables", i32),
+        (context_lens, "context_lens", i32), (workspace, "workspace", None),
+        (dev_err, "dev_err", i32))
+
+
+def pa_decode_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                 context_lens, scale: float, *, partition_size: int = 0,
+                 max_context_len: int = 0, reduce: str = "auto",
+                 workspace=None, dev_err=None, stream=None,
+                 desc: pa_decode_desc | None = None):
+    """``pa_decode`` over the 8-bit cache.  ``workspace`` (a uint8 CUDA
+    tensor of ``pa_decode_workspace_bytes`` bytes) is allocated per call when
+    not given.  Returns ``out``."""
+    lib = _lib.load()
+    if desc is None:
+        desc = make_desc(q, k_cache, block_tables,
+                         partition_size=partition_size,
+                         max_context_len=max_context_len, reduce=reduce)
+    _out_mode(desc, out, q.dtype)
+    if workspace is None:
+        workspace = _workspace(
+            int(lib.pa_decode_workspace_bytes(ctypes.byref(desc))), q.device,
+            stream)
+    p = _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
+                        block_tables, context_lens, workspace, dev_err)
+    st = lib.pa_decode_q8(
+        *p[:8], scale, ctypes.byref(desc), p[8],
+        workspace.numel() * workspace.element_size(), p[9], _stream(stream))
+    _lib.check(st, "pa_decode_q8")
+    return out
+
+
+def pa_copy_blocks_q8(k_cache, v_cache, k_scales, v_scales, pairs, *,
+                      dev_err=None, stream=None):
+    """``pa_copy_blocks`` for the 8-bit cache: codes and scales of block
+    pairs[i, 0] into block pairs[i, 1]."""
+    import torch
+    nb, hkv, bs, d = _check_q8(k_cache, v_cache, k_scales, v_scales)
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [num_pairs, 2]")
+    e4m3, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    p = _on_current((k_cache, "k_cache", e4m3), (v_cache, "v_cache", e4m3),
+                    (k_scales, "k_scales", f32), (v_scales, "v_scales", f32),
+                    (pairs, "pairs", i32), (dev_err, "dev_err", i32))
+    st = _lib.load().pa_copy_blocks_q8(*p[:5], pairs.shape[0], hkv, d, bs, nb,
+                                       p[5], _stream(stream))
+    _lib.check(st, "pa_copy_blocks_q8")
+
+
+def pa_swap_blocks_q8(dst_k, dst_v, dst_k_scales, dst_v_scales, src_k, src_v,
+                      src_k_scales, src_v_scales, pairs, *, dev_err=None,
+                      stream=None):
+    """``pa_swap_blocks`` for the 8-bit cache (codes and scales); any pool
+    (and ``pairs``) may be pinned CPU tensors."""
+    import torch
+    ns, hkv, bs, d = _check_q8(src_k, src_v, src_k_scales, src_v_scales,
+                               ("src ", ""))
+    nd, *rest = _check_q8(dst_k, dst_v, dst_k_scales, dst_v_scales,
+                          ("dst ", ""))
+    if tuple(rest) != (hkv, bs, d):
+        raise ValueError("the pools' blocks differ in shape")
+    if pairs.ndim != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n, 2]")
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    st = _lib.load().pa_swap_blocks_q8(
+        _reachable(dst_k, "dst_k", e4m3), _reachable(dst_v, "dst_v", e4m3),
+        _reachable(dst_k_scales, "dst_k_scales", f32),
+        _reachable(dst_v_scales, "dst_v_scales", f32),
+        _reachable(src_k, "src_k", e4m3), _reachable(src_v, "src_v", e4m3),
+        _reachable(src_k_scales, "src_k_scales", f32),
+        _reachable(src_v_scales, "src_v_scales", f32),
+        _reachable(pairs, "pairs", torch.int32), pairs.shape[0], hkv, d, bs,
+        ns, nd, _dev(dev_err, "dev_err", torch.int32), _stream(stream))
+    _lib.check(st, "pa_swap_blocks_q8")
+
+
+def pa_pool_blocks_q8(nbytes: int, num_layers: int, num_kv_heads: int,
+                      head_dim: int, block_size: int) -> int:
+    """``pa_pool_blocks`` for the 8-bit cache (codes and scales)."""
+    n = _lib.load().pa_pool_blocks_q8(int(nbytes), num_layers, num_kv_heads,
+                                      head_dim, block_size)
+    if n < 0:
+        _lib.check(_lib.PA_ERR_INVALID_ARG, "pa_pool_blocks_q8")
+    return n
 
 
 class BlockManager:

@@ -76,7 +76,45 @@ class pa_prefill_desc(ctypes.Structure):
     ]
 
 
+class pa_append_desc(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int),
+        ("num_q_heads", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("block_size", ctypes.c_int),
+        ("max_blocks_per_seq", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("total_q", ctypes.c_int),
+        ("max_q_len", ctypes.c_int),
+        ("rot_dim", ctypes.c_int),
+        ("rope_layout", ctypes.c_int),
+        ("rope_scale", ctypes.c_float),
+        ("norm_eps", ctypes.c_float),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64),
+    ]
+
+
+class pa_rope_desc(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int),
+        ("scaling", ctypes.c_int),
+        ("original_len", ctypes.c_int),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+    ]
+
+
 PA_PREFILL_AUTO, PA_PREFILL_TILE = 0, 1
+# pa_rope_layout, pa_rope_scaling
+PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_WAVELENGTH, PA_ROPE_YARN = 0, 1, 2, 3
 # pa_prefill_pv
 PA_PV_AUTO, PA_PV_SPLIT, PA_PV_SINGLE = 0, 1, 2
 
@@ -112,6 +150,19 @@ SIGNATURES = {
                              _vp, _vp]),
     "pa_swap_blocks": (_st, [_vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int,
                              _int, _int, _int, _vp, _vp]),
+    "pa_append": (_st, [_vp] * 12 + [ctypes.POINTER(pa_append_desc), _vp,
+                                     _vp]),
+    "pa_append_q8": (_st, [_vp] * 14 + [ctypes.POINTER(pa_append_desc), _vp,
+                                        _vp]),
+    "pa_rope_freqs": (_st, [ctypes.POINTER(pa_rope_desc),
+                            ctypes.POINTER(ctypes.c_double),
+                            ctypes.POINTER(ctypes.c_float)]),
+    "pa_decode_q8": (_st, [_vp] * 8 + [ctypes.c_float,
+                                       ctypes.POINTER(pa_decode_desc), _vp,
+                                       ctypes.c_size_t, _vp, _vp]),
+    "pa_copy_blocks_q8": (_st, [_vp] * 5 + [_int] * 5 + [_vp, _vp]),
+    "pa_swap_blocks_q8": (_st, [_vp] * 9 + [_int] * 6 + [_vp, _vp]),
+    "pa_pool_blocks_q8": (_i64, [ctypes.c_uint64, _int, _int, _int, _int]),
     "pa_bm_create": (_st, [_int, _int, _pi32, ctypes.POINTER(_vp)]),
     "pa_bm_destroy": (None, [_vp]),
     "pa_bm_add_seq": (_st, [_vp, _i64]),

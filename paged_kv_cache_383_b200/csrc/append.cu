@@ -1,0 +1,737 @@
+// pa_append and pa_append_q8: what a layer does with its new queries, keys and
+// values before attention, in one launch: the norm of each query and key head
+// (optional), the position rotation, and the write of K and V into the paged
+// cache, in the cache's own 16-bit type or as e4m3 codes with one scale for
+// each (block, KV head).
+//
+// Row t of sequence b (i-th of its q_len new tokens) sits at position
+// p = L_b - q_len + i, in block table[b][p / block_size].  With x a head:
+//   norm      x <- w x / sqrt(mean(x^2) + eps)
+//   rotation  (u, w) <- (u cos - w sin, w cos + u sin) for pair j of the first
+//             rot_dim elements, at the angle p f_j; the pairs are (j, j +
+//             rot_dim/2) or (2j, 2j + 1).
+// All in fp32 with one rounding at the end; the angle is reduced to a
+// fraction of a turn in fp64 (an fp32 product is off by a tenth of a radian at
+// position 10^6), so any position below 2^31 is exact to about 2^-24 turns
+// and no table is read.
+//
+// What bounds it: bytes (each element is read and written once; about ten
+// operations for each), or, for a decode step, the latency of the chain
+// lengths -> block id -> store.  The rows' loads do not depend on that chain
+// and are issued first; a token's sines and cosines are computed once per CTA
+// and shared by its heads.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "device_utils.cuh"
+#include "e4m3.cuh"
+#include "pagedkv.h"
+#include "status.h"
+
+namespace pagedkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWindow = 16;  // rows whose blocks one K/V CTA looks after
+constexpr int kMaxBlock = 32;   // block_size
+constexpr int kMaxPairs = 64;   // rotated pairs: head_dim / 2
+// Scales written by pa_append_q8: 2^e with e in this range.
+constexpr int kMinScaleExp = -64, kMaxScaleExp = 120;
+
+struct AppendArgs {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_norm;  // nullable
+  const void* k_norm;
+  const double* freqs;
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;  // pa_append_q8 only
+  float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;  // nullable: row t is sequence t's only one
+  int32_t* dev_err;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int num_seqs, num_q_heads, num_kv_heads;
+  int block_size, max_blocks_per_seq, num_blocks;
+  int total_q, max_q_len;
+  int rot_pairs;  // rot_dim / 2
+  int interleaved;
+  float rope_scale, norm_eps;
+  int row_splits;   // CTAs that share a token's rows
+  int kv_ctas;      // pa_append_q8: CTAs 0 .. kv_ctas - 1 write K and V
+  int window;       // rows per K/V window
+  int unit_groups;  // CTAs per window (kWarps (K or V, head) units each)
+};
+
+// Where a sequence's new rows are; `ok` false: nothing of it is written.
+struct Seq {
+  int q0, q_len, L;
+  bool ok;
+};
+__device__ __forceinline__ Seq read_seq(const AppendArgs& a, int b) {
+  Seq s;
+  s.q0 = a.query_start ? a.query_start[b] : b;
+  s.q_len = a.query_start ? a.query_start[b + 1] - s.q0 : 1;
+  s.L = a.context_lens[b];
+  s.ok = false;
+  if (s.L == 0) return s;  // padding
+  const bool bad =
+      s.L < 0 ||
+      s.L > static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size ||
+      s.q_len < 0 || s.q_len > s.L || s.q_len > a.max_q_len || s.q0 < 0 ||
+      s.q0 > a.total_q - s.q_len;
+  if (bad)
+    dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
+  else
+    s.ok = s.q_len > 0;
+  return s;
+}
+
+// cos and sin of the pair's angle at position p, times rope_scale.
+__device__ __forceinline__ float2 turn(const AppendArgs& a, int pair, int p) {
+  const double t = static_cast<double>(p) *
+                   (a.freqs[pair] * 0.15915494309189533577);  // 1 / (2 pi)
+  float s, c;
+  sincospif(2.f * static_cast<float>(t - rint(t)), &s, &c);
+  return make_float2(c * a.rope_scale, s * a.rope_scale);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = dev::Mma<T>::unpack(r[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// Norm (weight non-null) and rotation of a head row spread over LPR lanes,
+// lane c of them holding elements 8c .. 8c + 7.  cs: the row's cos/sin pairs
+// in shared memory.  rotate / weight may differ between a warp's rows; every
+// lane takes part in the shuffles.
+template <typename T, int D>
+__device__ __forceinline__ void norm_rotate(float (&x)[8], const T* weight,
+                                            bool rotate, const float2* cs,
+                                            const AppendArgs& a, int c) {
+  constexpr int LPR = D / 8;
+  if (a.q_norm || a.k_norm) {  // uniform over the grid
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int m = 1; m < LPR; m <<= 1)
+      ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    if (weight) {
+      const float r = rsqrtf(ss * (1.f / D) + a.norm_eps);
+      float w[8];
+      unpack8<T>(reinterpret_cast<const uint4*>(weight)[c], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+    }
+  }
+  if (a.rot_pairs == 0) return;
+  const int lane = threadIdx.x & 31;
+  if (a.interleaved) {
+    if (rotate && 4 * c < a.rot_pairs) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 z = cs[4 * c + i];
+        const float u = x[2 * i], w = x[2 * i + 1];
+        x[2 * i] = u * z.x - w * z.y;
+        x[2 * i + 1] = w * z.x + u * z.y;
+      }
+    }
+  } else {
+    // Chunk c's partners are chunk c +- rot_pairs / 8, in another lane.
+    const int half = a.rot_pairs / 8;
+    const bool in = c < 2 * half, second = c >= half;
+    const int src = in ? (second ? lane - half : lane + half) : lane;
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      y[e] = __shfl_sync(0xffffffffu, x[e], src);
+    if (rotate && in) {
+      const float2* z = cs + 8 * (second ? c - half : c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = x[e] * z[e].x + (second ? y[e] : -y[e]) * z[e].y;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(dev::Mma<T>::pack(x[0], x[1]), dev::Mma<T>::pack(x[2], x[3]),
+                    dev::Mma<T>::pack(x[4], x[5]),
+                    dev::Mma<T>::pack(x[6], x[7]));
+}
+
+// Rows that keep 16 bits: the query heads, and (16-bit cache) the key and
+// value heads, of one token; `split` of its row_splits CTAs.
+template <typename T, int D, bool kQ8>
+__device__ __forceinline__ void token_rows(const AppendArgs& a, int t,
+                                           int split, float2* cs) {
+  constexpr int LPR = D / 8;               // lanes per row
+  constexpr int kSlots = kThreads / LPR;   // rows per pass of the CTA
+  constexpr int kBatch = 4;                // passes in flight
+  __shared__ int s_b;
+  const int tid = threadIdx.x;
+  const int c = tid % LPR, slot = tid / LPR;
+  const int rows = a.num_q_heads + (kQ8 ? 0 : 2 * a.num_kv_heads);
+  const int step = kSlots * a.row_splits;
+  const int first = split * kSlots + slot;
+  // Element 8c of row r of this token.
+  auto src = [&](int r) -> const uint4* {
+    const T* p;
+    if (r < a.num_q_heads)
+      p = static_cast<const T*>(a.q) + t * a.q_stride + r * D;
+    else if (r < a.num_q_heads + a.num_kv_heads)
+      p = static_cast<const T*>(a.k) + t * a.k_stride +
+          (r - a.num_q_heads) * D;
+    else
+      p = static_cast<const T*>(a.v) + t * a.v_stride +
+          (r - a.num_q_heads - a.num_kv_heads) * D;
+    return reinterpret_cast<const uint4*>(p) + c;
+  };
+  uint4 raw[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u)
+    if (first + u * step < rows) raw[u] = *src(first + u * step);
+
+  int b = t;
+  if (a.query_start) {
+    if (tid == 0) s_b = -1;
+    __syncthreads();
+    for (int j = tid; j < a.num_seqs; j += kThreads)
+      if (a.query_start[j] <= t && t < a.query_start[j + 1]) s_b = j;
+    __syncthreads();
+    b = s_b;
+    if (b < 0) return;  // a row behind the last sequence: left as it was
+  }
+  const Seq sq = read_seq(a, b);
+  if (!sq.ok) return;
+  const int pos = sq.L - sq.q_len + t - sq.q0;
+  int blk = 0;
+  if constexpr (!kQ8) {
+    blk = a.block_tables[static_cast<int64_t>(b) * a.max_blocks_per_seq +
+                         pos / a.block_size];
+    if (blk < 0 || blk >= a.num_blocks) {
+      if (tid == 0) dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
+      blk = -1;
+    }
+  }
+  if (tid < a.rot_pairs) cs[tid] = turn(a, tid, pos);
+  __syncthreads();
+
+  const int64_t page = static_cast<int64_t>(blk) * a.num_kv_heads;
+  for (int r0 = first; r0 - slot < rows; r0 += kBatch * step) {
+    if (r0 != first) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (r0 + u * step < rows) raw[u] = *src(r0 + u * step);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = r0 + u * step;
+      if (r - slot >= rows) break;  // uniform over the CTA
+      const bool is_q = r < a.num_q_heads;
+      const int kv = r - a.num_q_heads;  // key heads, then value heads
+      const bool is_v = kv >= a.num_kv_heads;
+      float x[8] = {};
+      if (r < rows) unpack8<T>(raw[u], x);
+      norm_rotate<T, D>(x,
+                        static_cast<const T*>(is_q ? a.q_norm
+                                              : is_v ? nullptr : a.k_norm),
+                        is_q || !is_v, cs, a, c);
+      if (r >= rows) continue;
+      T* dst;
+      if (is_q) {
+        dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + r * D;
+      } else {
+        if (blk < 0) continue;
+        const int h = is_v ? kv - a.num_kv_heads : kv;
+        dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) +
+              ((page + h) * a.block_size + pos % a.block_size) * D;
+      }
+      // V unchanged: the very bits (a NaN's payload too).
+      reinterpret_cast<uint4*>(dst)[c] =
+          !is_q && is_v ? raw[u] : pack8<T>(x);
+    }
+  }
+}
+
+// The smallest power of two s with amax <= 448 s, from amax's bits: with
+// amax = 2^x m, 448 = 2^8 * 1.75.
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t w = __float_as_uint(amax);
+  const int e = static_cast<int>(w >> 23) - 127 - 8 +
+                ((w & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return dev::exp2_int(max(kMinScaleExp, min(kMaxScaleExp, e)));
+}
+
+// One warp: new rows [row, row + n) of one sequence, all in block `blk` from
+// offset o on, of one KV head's K (weight / rotation) or V, into codes and
+// the scale.  The warp alone touches this (block, head).
+template <typename T, int D>
+__device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
+                                              int h, int row, int n, int blk,
+                                              int o, const float2* cs) {
+  constexpr int LPR = D / 8, kRows = 32 / LPR;  // rows per pass
+  constexpr int kKeep = 4;                      // passes held in registers
+  const int lane = threadIdx.x & 31;
+  const int c = lane % LPR, sub = lane / LPR;
+  const T* base = is_k ? static_cast<const T*>(a.k) + row * a.k_stride
+                       : static_cast<const T*>(a.v) + row * a.v_stride;
+  const int64_t stride = is_k ? a.k_stride : a.v_stride;
+  const T* weight = is_k ? static_cast<const T*>(a.k_norm) : nullptr;
+  const int64_t unit = static_cast<int64_t>(blk) * a.num_kv_heads + h;
+  float* sp = (is_k ? a.k_scales : a.v_scales) + unit;
+  const float s_old = o > 0 ? *sp : 0.f;
+  uint8_t* page = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) +
+                  unit * a.block_size * D;
+  auto load = [&](int r) {
+    return r < n ? reinterpret_cast<const uint4*>(base + r * stride + h * D)[c]
+                 : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto value = [&](const uint4& raw, int r, float (&x)[8]) {
+    unpack8<T>(raw, x);
+    if (is_k)  // uniform over the warp
+      norm_rotate<T, D>(x, weight, true,
+                        cs + min(r, n - 1) * a.rot_pairs, a, c);
+  };
+  float amax = 0.f;
+  float kept[kKeep][8];
+  const int passes = (n + kRows - 1) / kRows;
+  // Up to kKeep passes stay in registers; longer runs (a whole block of a
+  // prompt) are read and rotated twice, the second time from L1: holding 32
+  // rows of 128 would take 128 registers a lane.
+  for (int p0 = 0; p0 < passes; p0 += kKeep) {
+    uint4 raw[kKeep];
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) raw[u] = load((p0 + u) * kRows + sub);
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+      if (p0 + u >= passes) break;
+      value(raw[u], (p0 + u) * kRows + sub, kept[u]);
+      if ((p0 + u) * kRows + sub < n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(kept[u][e]));
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1)
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+  const float s = fmaxf(s_old, scale_for(amax));
+  if (lane == 0 && s != s_old) *sp = s;
+  if (o > 0 && s > s_old) {
+    // Older codes of the block follow the scale: exact for powers of two but
+    // where a code becomes subnormal.
+    const float ratio = s_old / s;
+    uint4* old = reinterpret_cast<uint4*>(page);
+    for (int i = lane; i < o * (D / 16); i += 32) {
+      uint4 w = old[i];
+      uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = dev::e4m3x2_to_f16x2(r[e]);
+        const uint32_t hi = dev::e4m3x2_to_f16x2_hi(r[e]);
+        const float2 f = dev::Mma<__half>::unpack(lo);
+        const float2 g = dev::Mma<__half>::unpack(hi);
+        r[e] = dev::f32x4_to_e4m3x4(f.x * ratio, f.y * ratio, g.x * ratio,
+                                    g.y * ratio);
+      }
+      old[i] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+  // x / s; times the reciprocal where that is exact (a power of two).
+  const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0u;
+  const float inv = 1.f / s;
+  auto store = [&](const float (&x)[8], int r) {
+    if (r >= n) return;
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = pow2 ? x[e] * inv : x[e] / s;
+    *reinterpret_cast<uint2*>(page + static_cast<int64_t>(o + r) * D + 8 * c) =
+        make_uint2(dev::f32x4_to_e4m3x4(y[0], y[1], y[2], y[3]),
+                   dev::f32x4_to_e4m3x4(y[4], y[5], y[6], y[7]));
+  };
+  for (int p0 = 0; p0 < passes; p0 += kKeep) {
+    if (passes > kKeep) {
+      uint4 raw[kKeep];
+#pragma unroll
+      for (int u = 0; u < kKeep; ++u) raw[u] = load((p0 + u) * kRows + sub);
+#pragma unroll
+      for (int u = 0; u < kKeep; ++u) {
+        if (p0 + u >= passes) break;
+        value(raw[u], (p0 + u) * kRows + sub, kept[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+      if (p0 + u >= passes) break;
+      store(kept[u], (p0 + u) * kRows + sub);
+    }
+  }
+}
+
+// K and V of the runs of rows that start a block (or their sequence) in rows
+// [window * w, window * (w + 1)): each run lies in one block.
+template <typename T, int D>
+__device__ __forceinline__ void window_kv(const AppendArgs& a, int w,
+                                          int group, float2* cs) {
+  __shared__ int s_run[kMaxWindow][2];  // sequence, first row
+  __shared__ int s_n;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int64_t lo64 = static_cast<int64_t>(w) * a.window;
+  const int lo = static_cast<int>(lo64);
+  const int hi = static_cast<int>(
+      min(lo64 + a.window, static_cast<int64_t>(a.total_q)));
+  if (tid == 0) s_n = 0;
+  __syncthreads();
+  auto push = [&](int b, int row) {
+    const int i = atomicAdd(&s_n, 1);
+    if (i < kMaxWindow) {
+      s_run[i][0] = b;
+      s_run[i][1] = row;
+    } else {  // sequences whose rows overlap
+      dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
+    }
+  };
+  if (!a.query_start) {
+    for (int t = lo + tid; t < hi; t += kThreads) push(t, t);
+  } else {
+    for (int j = tid; j < a.num_seqs; j += kThreads) {
+      const int q0 = a.query_start[j], q1 = a.query_start[j + 1];
+      if (q1 <= lo || q0 >= hi) continue;
+      const Seq sq = read_seq(a, j);
+      if (!sq.ok) continue;
+      const int from = max(q0, lo);
+      if (from == q0) push(j, q0);
+      // then the rows at a block's first slot
+      const int p = sq.L - sq.q_len + from - q0;
+      int r = from + (a.block_size - p % a.block_size) % a.block_size;
+      if (r == q0) r += a.block_size;
+      for (; r < min(hi, q1); r += a.block_size) push(j, r);
+    }
+  }
+  __syncthreads();
+  const int runs = min(s_n, kMaxWindow);
+  const int unit = group * kWarps + warp;
+  const bool any_k = group * kWarps < a.num_kv_heads;
+  for (int i = 0; i < runs; ++i) {
+    const int b = s_run[i][0], row = s_run[i][1];
+    const Seq sq = read_seq(a, b);
+    if (!sq.ok) continue;  // uniform
+    const int pos = sq.L - sq.q_len + row - sq.q0;
+    const int o = pos % a.block_size;
+    const int n = min(a.block_size - o, sq.q0 + sq.q_len - row);
+    const int blk =
+        a.block_tables[static_cast<int64_t>(b) * a.max_blocks_per_seq +
+                       pos / a.block_size];
+    if (blk < 0 || blk >= a.num_blocks) {
+      if (tid == 0) dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
+      continue;  // uniform
+    }
+    if (any_k) {
+      __syncthreads();  // the previous run's sines are read
+      for (int j = tid; j < n * a.rot_pairs; j += kThreads) {
+        const int r = j / a.rot_pairs;
+        cs[j] = turn(a, j - r * a.rot_pairs, pos + r);
+      }
+      __syncthreads();
+    }
+    if (unit < 2 * a.num_kv_heads) {
+      const bool is_k = unit < a.num_kv_heads;
+      quantise_unit<T, D>(a, is_k, is_k ? unit : unit - a.num_kv_heads, row,
+                          n, blk, o, cs);
+    }
+  }
+}
+
+template <typename T, int D, bool kQ8>
+__global__ void __launch_bounds__(kThreads)
+    append_kernel(const AppendArgs a) {
+  // cos/sin: one token's pairs, or those of a block's tokens.
+  __shared__ float2 cs[kQ8 ? kMaxBlock * (D / 2) : kMaxPairs];
+  dev::pdl_trigger();  // a following attention may run its prologue now
+  dev::pdl_wait();     // q, k and v may be the previous kernel's output
+  if (kQ8 && static_cast<int>(blockIdx.x) < a.kv_ctas) {
+    window_kv<T, D>(a, blockIdx.x / a.unit_groups, blockIdx.x % a.unit_groups,
+                    cs);
+  } else {
+    const unsigned i = blockIdx.x - (kQ8 ? a.kv_ctas : 0);
+    token_rows<T, D, kQ8>(a, i / a.row_splits, i % a.row_splits, cs);
+  }
+}
+
+pa_status check_append(const char* fn, const pa_append_desc* d) {
+  if (!d) return fail(PA_ERR_INVALID_ARG, "%s: desc is NULL", fn);
+  if (d->num_seqs < 0 || d->num_q_heads < 0 || d->num_kv_heads <= 0 ||
+      d->max_blocks_per_seq <= 0 || d->num_blocks < 0 || d->total_q < 0 ||
+      d->max_q_len < 0 || (d->dtype != PA_F16 && d->dtype != PA_BF16))
+    return fail(PA_ERR_INVALID_ARG,
+                "%s: num_seqs=%d num_q_heads=%d num_kv_heads=%d "
+                "max_blocks_per_seq=%d num_blocks=%d total_q=%d max_q_len=%d "
+                "dtype=%d", fn, d->num_seqs, d->num_q_heads, d->num_kv_heads,
+                d->max_blocks_per_seq, d->num_blocks, d->total_q,
+                d->max_q_len, static_cast<int>(d->dtype));
+  if ((d->head_dim != 64 && d->head_dim != 128) ||
+      (d->block_size != 16 && d->block_size != 32))
+    return fail(PA_ERR_UNSUPPORTED,
+                "%s: needs head_dim 64 or 128 (got %d) and block_size 16 or "
+                "32 (got %d)", fn, d->head_dim, d->block_size);
+  if (d->rot_dim < 0 || d->rot_dim > d->head_dim)
+    return fail(PA_ERR_INVALID_ARG, "%s: rot_dim %d not in 0 .. head_dim %d",
+                fn, d->rot_dim, d->head_dim);
+  if (d->rot_dim % 16)
+    return fail(PA_ERR_UNSUPPORTED, "%s: rot_dim %d is not a multiple of 16",
+                fn, d->rot_dim);
+  if (d->rope_layout != PA_ROPE_HALF && d->rope_layout != PA_ROPE_INTERLEAVED)
+    return fail(PA_ERR_INVALID_ARG, "%s: rope_layout %d", fn, d->rope_layout);
+  if (!std::isfinite(d->rope_scale) || !std::isfinite(d->norm_eps) ||
+      d->norm_eps < 0.f)
+    return fail(PA_ERR_INVALID_ARG, "%s: rope_scale or norm_eps", fn);
+  if (static_cast<int64_t>(d->max_blocks_per_seq) * d->block_size >
+      0x7fffffffLL)
+    return fail(PA_ERR_INVALID_ARG, "%s: max_blocks_per_seq too large", fn);
+  const int64_t strides[4] = {d->q_stride, d->k_stride, d->v_stride,
+                              d->q_out_stride};
+  const char* names[4] = {"q_stride", "k_stride", "v_stride", "q_out_stride"};
+  for (int i = 0; i < 4; ++i) {
+    const bool is_q = i == 0 || i == 3;
+    if (is_q && d->num_q_heads == 0) continue;
+    const int64_t row = static_cast<int64_t>(is_q ? d->num_q_heads
+                                                  : d->num_kv_heads) *
+                        d->head_dim;
+    if (strides[i] % 8 || (d->total_q > 1 && strides[i] < row))
+      return fail(PA_ERR_INVALID_ARG,
+                  "%s: %s %lld must be a multiple of 8 elements and at least "
+                  "a row (%lld)", fn, names[i],
+                  static_cast<long long>(strides[i]),
+                  static_cast<long long>(row));
+  }
+  return PA_OK;
+}
+
+template <typename T, int D, bool kQ8>
+pa_status launch(const char* fn, const AppendArgs& a, int64_t ctas,
+                 cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, append_kernel<T, D, kQ8>, a);
+  count_launch();
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess)
+    return fail(PA_ERR_CUDA, "%s: launch failed: %s", fn,
+                cudaGetErrorString(e));
+  return PA_OK;
+}
+
+template <bool kQ8>
+pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
+                 float* k_scales, float* v_scales, const void* q,
+                 const void* k, const void* v, const void* q_norm,
+                 const void* k_norm, const double* rope_freqs,
+                 const int32_t* block_tables, const int32_t* context_lens,
+                 const int32_t* query_start, const pa_append_desc* d,
+                 int32_t* dev_err, void* stream) {
+  clear_error();
+  const pa_status st = check_append(fn, d);
+  if (st != PA_OK) return st;
+  if (!query_start && d->total_q != d->num_seqs)
+    return fail(PA_ERR_INVALID_ARG,
+                "%s: without query_start every sequence has one row, but "
+                "total_q %d != num_seqs %d", fn, d->total_q, d->num_seqs);
+  if (d->num_seqs == 0 || d->total_q == 0 || d->max_q_len == 0) return PA_OK;
+  if (!k_cache || !v_cache || !k || !v || !block_tables || !context_lens ||
+      (d->num_q_heads > 0 && (!q || !q_out)) ||
+      (kQ8 && (!k_scales || !v_scales)))
+    return fail(PA_ERR_INVALID_ARG, "%s: NULL tensor pointer", fn);
+  if (d->rot_dim > 0 && !rope_freqs)
+    return fail(PA_ERR_INVALID_ARG, "%s: rot_dim %d without rope_freqs", fn,
+                d->rot_dim);
+  const void* aligned[8] = {q_out, k_cache, v_cache, q, k, v, q_norm, k_norm};
+  for (const void* p : aligned)
+    if (!aligned16(p))
+      return fail(PA_ERR_INVALID_ARG,
+                  "%s: q, k, v, q_out, the norm weights and the caches must "
+                  "be 16-byte aligned", fn);
+  if (d->num_blocks == 0)
+    return fail(PA_ERR_INVALID_ARG, "%s: empty block pool", fn);
+  AppendArgs a;
+  a.q_out = q_out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_norm = d->num_q_heads > 0 ? q_norm : nullptr;
+  a.k_norm = k_norm;
+  a.freqs = rope_freqs;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.dev_err = dev_err;
+  a.q_stride = d->q_stride;
+  a.k_stride = d->k_stride;
+  a.v_stride = d->v_stride;
+  a.q_out_stride = d->q_out_stride;
+  a.num_seqs = d->num_seqs;
+  a.num_q_heads = d->num_q_heads;
+  a.num_kv_heads = d->num_kv_heads;
+  a.block_size = d->block_size;
+  a.max_blocks_per_seq = d->max_blocks_per_seq;
+  a.num_blocks = d->num_blocks;
+  a.total_q = d->total_q;
+  a.max_q_len = d->max_q_len;
+  a.rot_pairs = d->rot_dim / 2;
+  a.interleaved = d->rope_layout == PA_ROPE_INTERLEAVED;
+  a.rope_scale = d->rope_scale;
+  a.norm_eps = d->norm_eps;
+  // Rows of one token: one CTA takes them in passes of 16 (head_dim 128) or
+  // 32; with few tokens its passes are dealt out to several CTAs, as long as
+  // the grid stays within about four CTAs per SM.
+  const int slots = kThreads / (d->head_dim / 8);
+  const int rows = d->num_q_heads + (kQ8 ? 0 : 2 * d->num_kv_heads);
+  const int passes = (rows + slots - 1) / slots;
+  const int64_t room = 4LL * device_sm_count();
+  a.row_splits = static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>(passes, room / d->total_q)));
+  int64_t ctas = static_cast<int64_t>(d->total_q) * a.row_splits;
+  if (rows == 0) ctas = 0;
+  a.kv_ctas = 0;
+  a.window = 1;
+  a.unit_groups = 1;
+  if (kQ8) {
+    // A window of one row per CTA when every row starts a run (a decode
+    // step) or rows are few; with many rows most start none, and windows of
+    // up to 16 rows keep the CTAs that find nothing to do few.
+    a.unit_groups = (2 * d->num_kv_heads + kWarps - 1) / kWarps;
+    const int64_t units = static_cast<int64_t>(d->total_q) * a.unit_groups;
+    while (query_start && a.window < kMaxWindow &&
+           units / a.window > 8LL * device_sm_count())
+      a.window *= 2;
+    const int64_t windows = (d->total_q + a.window - 1) / a.window;
+    if (windows * a.unit_groups + ctas > 0x7fffffffLL)
+      return fail(PA_ERR_UNSUPPORTED, "%s: %d rows are too many", fn,
+                  d->total_q);
+    a.kv_ctas = static_cast<int>(windows * a.unit_groups);
+    ctas += a.kv_ctas;
+  }
+  if (ctas > 0x7fffffffLL)
+    return fail(PA_ERR_UNSUPPORTED, "%s: %d rows are too many", fn,
+                d->total_q);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->dtype == PA_BF16)
+    return d->head_dim == 128
+               ? launch<__nv_bfloat16, 128, kQ8>(fn, a, ctas, s)
+               : launch<__nv_bfloat16, 64, kQ8>(fn, a, ctas, s);
+  return d->head_dim == 128 ? launch<__half, 128, kQ8>(fn, a, ctas, s)
+                            : launch<__half, 64, kQ8>(fn, a, ctas, s);
+}
+
+}  // namespace
+}  // namespace pagedkv
+
+using pagedkv::fail;
+
+extern "C" {
+
+pa_status pa_append(void* q_out, void* k_cache, void* v_cache, const void* q,
+                    const void* k, const void* v, const void* q_norm,
+                    const void* k_norm, const double* rope_freqs,
+                    const int32_t* block_tables, const int32_t* context_lens,
+                    const int32_t* query_start, const pa_append_desc* desc,
+                    int32_t* dev_err, void* stream) {
+  return pagedkv::append<false>("pa_append", q_out, k_cache, v_cache, nullptr,
+                                nullptr, q, k, v, q_norm, k_norm, rope_freqs,
+                                block_tables, context_lens, query_start, desc,
+                                dev_err, stream);
+}
+
+pa_status pa_append_q8(void* q_out, void* k_cache, void* v_cache,
+                       float* k_scales, float* v_scales, const void* q,
+                       const void* k, const void* v, const void* q_norm,
+                       const void* k_norm, const double* rope_freqs,
+                       const int32_t* block_tables,
+                       const int32_t* context_lens,
+                       const int32_t* query_start, const pa_append_desc* desc,
+                       int32_t* dev_err, void* stream) {
+  return pagedkv::append<true>("pa_append_q8", q_out, k_cache, v_cache,
+                               k_scales, v_scales, q, k, v, q_norm, k_norm,
+                               rope_freqs, block_tables, context_lens,
+                               query_start, desc, dev_err, stream);
+}
+
+// Host only: the angular frequencies of the rotation (see pagedkv.h).
+pa_status pa_rope_freqs(const pa_rope_desc* d, double* freqs_out,
+                        float* scale_out) {
+  pagedkv::clear_error();
+  if (!d || !freqs_out || !scale_out)
+    return fail(PA_ERR_INVALID_ARG, "pa_rope_freqs: NULL pointer");
+  if (d->rot_dim <= 0 || d->rot_dim % 2 || !(d->base > 1.0) ||
+      !std::isfinite(d->base))
+    return fail(PA_ERR_INVALID_ARG, "pa_rope_freqs: rot_dim=%d base=%g",
+                d->rot_dim, d->base);
+  const bool scaled = d->scaling != PA_ROPE_PLAIN;
+  const bool banded = d->scaling == PA_ROPE_WAVELENGTH ||
+                      d->scaling == PA_ROPE_YARN;
+  if (d->scaling < PA_ROPE_PLAIN || d->scaling > PA_ROPE_YARN ||
+      (scaled && !(std::isfinite(d->factor) && d->factor >= 1.0)) ||
+      (banded && (d->original_len <= 0 || !(d->low > 0.0) ||
+                  !(d->high > d->low) || !std::isfinite(d->high))))
+    return fail(PA_ERR_INVALID_ARG,
+                "pa_rope_freqs: scaling=%d factor=%g original_len=%d low=%g "
+                "high=%g", d->scaling, d->factor, d->original_len, d->low,
+                d->high);
+  const double two_pi = 6.283185307179586477;
+  // Yarn's ramp over the pairs: pair(r) turns r times in original_len.
+  double first = 0.0, last = 0.0;
+  if (d->scaling == PA_ROPE_YARN) {
+    auto pair = [&](double turns) {
+      return d->rot_dim * std::log(d->original_len / (turns * two_pi)) /
+             (2.0 * std::log(d->base));
+    };
+    first = std::max(std::floor(pair(d->high)), 0.0);
+    last = std::min(std::ceil(pair(d->low)), d->rot_dim - 1.0);
+    if (last <= first) last = first + 0.001;
+  }
+  for (int j = 0; j < d->rot_dim / 2; ++j) {
+    const double f = std::pow(d->base, -2.0 * j / d->rot_dim);
+    double w = 0.0;  // how much of f is divided by the factor
+    if (d->scaling == PA_ROPE_LINEAR) {
+      w = 1.0;
+    } else if (d->scaling == PA_ROPE_WAVELENGTH) {
+      const double turns = d->original_len * f / two_pi;
+      w = std::min(1.0, std::max(0.0, (d->high - turns) / (d->high - d->low)));
+    } else if (d->scaling == PA_ROPE_YARN) {
+      w = std::min(1.0, std::max(0.0, (j - first) / (last - first)));
+    }
+    freqs_out[j] = scaled ? w * (f / d->factor) + (1.0 - w) * f : f;
+  }
+  *scale_out = d->scaling == PA_ROPE_YARN && d->factor > 1.0
+                   ? static_cast<float>(0.1 * std::log(d->factor) + 1.0)
+                   : 1.f;
+  return PA_OK;
+}
+
+}  // extern "C"

@@ -514,6 +514,23 @@ int64_t pa_pool_blocks(uint64_t bytes, int num_layers, int num_kv_heads,
   return static_cast<int64_t>(bytes / per_block);
 }
 
+int64_t pa_pool_blocks_q8(uint64_t bytes, int num_layers, int num_kv_heads,
+                          int head_dim, int block_size) {
+  pagedkv::clear_error();
+  if (num_layers <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      block_size <= 0) {
+    fail(PA_ERR_INVALID_ARG,
+         "pa_pool_blocks_q8: num_layers=%d num_kv_heads=%d head_dim=%d "
+         "block_size=%d", num_layers, num_kv_heads, head_dim, block_size);
+    return -1;
+  }
+  // K and V, every layer, every KV head: block_size rows of codes, a scale.
+  const uint64_t per_block = 2ull * num_layers * num_kv_heads *
+                             (static_cast<uint64_t>(head_dim) * block_size +
+                              sizeof(float));
+  return static_cast<int64_t>(bytes / per_block);
+}
+
 int pa_bm_refcount(void* p, int block) {
   BlockManager* bm = as_bm(p);
   if (!bm || block < 0 || block >= bm->num_blocks) return -1;

@@ -60,6 +60,25 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+void* device_view(const void* p) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();  // the failed query's error is not sticky: clear it
+    return nullptr;
+  }
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  switch (a.type) {
+    case cudaMemoryTypeDevice:
+    case cudaMemoryTypeManaged:
+      return a.device == dev ? const_cast<void*>(p) : nullptr;
+    case cudaMemoryTypeHost:
+      return a.devicePointer;  // NULL if the allocation is not mapped
+    default:
+      return nullptr;
+  }
+}
+
 }  // namespace pagedkv
 
 extern "C" {

@@ -28,6 +28,11 @@ int device_sm_count();
 // The driver's cuTensorMapEncodeTiled, or nullptr if it is unavailable.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// Address at which the current device reaches `p`: device memory of this
+// device, or mapped page-locked host memory.  nullptr for anything else
+// (pageable host memory, another device's memory).
+void* device_view(const void* p);
+
 inline bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }

@@ -58,28 +58,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Address at which the current device reaches `p`: device memory of this
-// device, or mapped page-locked host memory.  nullptr for anything else
-// (pageable host memory, another device's memory).
-void* device_view(const void* p) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();  // the failed query's error is not sticky: clear it
-    return nullptr;
-  }
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  switch (a.type) {
-    case cudaMemoryTypeDevice:
-    case cudaMemoryTypeManaged:
-      return a.device == dev ? const_cast<void*>(p) : nullptr;
-    case cudaMemoryTypeHost:
-      return a.devicePointer;  // NULL if the allocation is not mapped
-    default:
-      return nullptr;
-  }
-}
-
 }  // namespace
 }  // namespace pagedkv
 

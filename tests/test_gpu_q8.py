@@ -1,0 +1,317 @@
+"""Attention over the 8-bit cache, and its block moves, against the fp64
+oracle on the values that the codes and scales stand for.
+
+Tolerance on the float32 output, per element: the weights enter the second
+product in fp16, each off by at most 2^-11 of itself (bf16 outputs; twice the
+half step 2^-12 for the normalisation by their exact sum), or with its
+residual by 2^-22 (fp16 outputs); scores and exponentials in fp32 move a weight
+by less than 2^-16 (arguments below 2^7 rounded at 2^-24, 128 products
+accumulated in fp32).  Both act on sum p |v|:
+  |err| <= (2^-11 or 2^-22, + 2^-15) * sum_t p_t |v_t|  + tiny.
+The 16-bit output must be the float32 one's rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as oa
+from paged_kv_cache_383_b200 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+BF, HF = torch.bfloat16, torch.float16
+
+
+def to64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+class Pool:
+    """A random 8-bit pool and tables for given contexts; slots and blocks
+    that no sequence wrote hold NaN codes, their scales NaN."""
+
+    def __init__(self, hkv, d, bs, ctx, *, seed=0, pow2=True, spread=2.0,
+                 extra=4):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.ctx = np.array(ctx, dtype=np.int32)
+        nblk = -(-self.ctx // bs)
+        need = int(nblk.sum())
+        self.n = need + extra
+        perm = rng.permutation(self.n).astype(np.int32)
+        self.table = np.full((len(ctx), max(int(nblk.max()), 1)), -1,
+                             dtype=np.int32)
+        at, used = 0, np.zeros((self.n, bs), dtype=bool)
+        for b, c in enumerate(nblk):
+            self.table[b, :c] = perm[at:at + c]
+            at += c
+            for i, blk in enumerate(self.table[b, :c]):
+                used[blk, :min(bs, int(ctx[b]) - i * bs)] = True
+        shape = (self.n, hkv, bs, d)
+        u = torch.from_numpy(used).cuda()[:, None, :, None]
+        self.t = []
+        for _ in "kv":
+            c = (torch.randn(shape, generator=g, device="cuda") * 100).clamp(
+                -448, 448)
+            c = torch.where(u, c, torch.full_like(c, float("nan"))).to(E4M3)
+            e = torch.randn(shape[:2], generator=g, device="cuda") * spread
+            s = 2.0 ** (torch.round(e) if pow2 else e) / 100
+            if pow2:
+                s = 2.0 ** torch.round(torch.log2(s))
+            s = torch.where(u.any(2)[..., 0].expand_as(s), s,
+                            torch.full_like(s, float("nan")))
+            self.t.append((c, s.contiguous()))
+        (self.kc, self.ks), (self.vc, self.vs) = self.t
+        self.cache = (self.kc, self.vc, self.ks, self.vs)
+        self.dev = [torch.from_numpy(x).cuda() for x in (self.table,
+                                                         self.ctx)]
+
+    def values(self):
+        """fp64 K and V pools (NaN where nothing was written)."""
+        return [to64(c) * to64(s)[:, :, None, None] for c, s in self.t]
+
+
+def reference(pool, q, qpos, scale):
+    """fp64 output and sum p |v| of each query row; qpos: (sequence, last
+    visible position) per row."""
+    kv, vv = pool.values()
+    q = to64(q)
+    hq, hkv = q.shape[1], kv.shape[1]
+    out, mag = np.zeros_like(q), np.zeros_like(q)
+    bs = kv.shape[2]
+    for r, (b, p) in enumerate(qpos):
+        if p < 0:
+            continue
+        for h in range(hkv):
+            K = oa.depage(kv, pool.table[b], p + 1, h, bs)
+            V = oa.depage(vv, pool.table[b], p + 1, h, bs)
+            for g in range(h * hq // hkv, (h + 1) * hq // hkv):
+                out[r, g] = oa.attend(q[r, g], K, V, scale)
+                mag[r, g] = oa.attend(q[r, g], K, np.abs(V), scale)
+    return out, mag
+
+
+def check(out32, out, ref, mag, dtype, rows=None):
+    got = to64(out32)
+    rel = (2.0 ** -11 if dtype == BF else 2.0 ** -22) + 2.0 ** -15
+    ok = np.abs(got - ref) <= rel * mag + 1e-30
+    if rows is not None:
+        ok = ok[rows]
+        assert torch.equal(out[rows], out32.to(dtype)[rows])
+    else:
+        assert torch.equal(out, out32.to(dtype))
+    assert ok.all(), float((np.abs(got - ref) / (mag + 1e-30)).max())
+
+
+def decode(pkv, pool, q, scale, **kw):
+    out32 = torch.full(q.shape, float("nan"), device="cuda")
+    out = torch.empty_like(q)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for o in (out32, out):
+        pkv.pa_decode_q8(o, q, *pool.cache, *pool.dev, scale, dev_err=err,
+                         **kw)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    return out32, out
+
+
+DECODE = [
+    # dtype, hq, hkv, d, bs, ctx, kw
+    (BF, 8, 8, 64, 16, [1], {}),
+    (HF, 8, 8, 64, 16, [47, 612, 130, 1900], {}),
+    (BF, 16, 2, 128, 16, [0, 1, 15, 16, 17, 100, 0], {}),
+    (HF, 16, 2, 128, 32, [31, 32, 33, 1, 700], {}),
+    (BF, 6, 2, 64, 32, [5, 90, 64], {}),
+    (HF, 7, 1, 128, 16, [333, 2], {}),
+    (BF, 64, 8, 128, 16, [900, 3, 1200], {"partition_size": 64}),
+    (BF, 64, 8, 128, 16, [900, 3, 1200],
+     {"partition_size": 64, "reduce": "kernel"}),
+    (HF, 32, 8, 128, 32, [2049, 512, 513],
+     {"partition_size": 512, "reduce": "kernel"}),
+    (BF, 8, 1, 128, 16, [5000], {"partition_size": 16}),
+    (HF, 4, 4, 64, 16, [3000, 700], {"partition_size": 2048,
+                                     "reduce": "kernel"}),
+    (BF, 8, 2, 64, 32, [4100, 2050], {"max_context_len": 4100}),
+]
+
+
+@pytest.mark.parametrize("case", DECODE,
+                         ids=lambda c: f"{c[1]}x{c[2]}x{c[3]}-{c[4]}")
+@pytest.mark.parametrize("pow2", [True, False])
+def test_decode(pkv, case, pow2):
+    dtype, hq, hkv, d, bs, ctx, kw = case
+    pool = Pool(hkv, d, bs, ctx, seed=len(ctx), pow2=pow2)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(len(ctx), hq, d, generator=g, device="cuda").to(dtype)
+    scale = d ** -0.5
+    out32, out = decode(pkv, pool, q, scale, **kw)
+    ref, mag = reference(pool, q, [(b, c - 1) for b, c in enumerate(ctx)],
+                         scale)
+    check(out32, out, ref, mag, dtype)
+    assert (to64(out)[np.array(ctx) == 0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_decode_wide_ranges(pkv, dtype):
+    """Scales of V that span 60 binades block by block, blocks of zeros with
+    scale 0 among them, large and tiny queries, peaked scores."""
+    ctx = [300, 77]
+    pool = Pool(2, 128, 16, ctx, seed=8)
+    n = pool.n
+    e = torch.arange(n, device="cuda") * 37 % 61 - 30
+    ok = ~torch.isnan(pool.vs)
+    pool.vs.copy_(torch.where(ok, torch.exp2(e.float())[:, None].expand(n, 2),
+                              pool.vs))
+    for b in (int(pool.table[0, 3]), int(pool.table[1, 0])):
+        pool.vc[b] = torch.zeros_like(pool.vc[b].float()).to(E4M3)
+        pool.vs[b] = 0.0
+    b = int(pool.table[0, 5])
+    pool.kc[b] = torch.zeros_like(pool.kc[b].float()).to(E4M3)
+    pool.ks[b] = 0.0
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn(2, 16, 128, generator=g, device="cuda")
+    q[:, 3] *= 50
+    q[:, 4] *= 2.0 ** -13
+    q[:, 5] = 0
+    q[:, 6, 7] = 300  # one large element among small ones
+    q = q.to(dtype)
+    out32, out = decode(pkv, pool, q, 0.05)
+    ref, mag = reference(pool, q, [(0, 299), (1, 76)], 0.05)
+    got = to64(out32)
+    # 300 / 50 times larger scores: arguments to 2^10, so 2^-13 on a weight;
+    # and a weight below 2^-24 of the largest v in reach is rounded to it
+    vmax = np.array([np.nanmax(np.abs(np.stack(
+        [pool.values()[1][blk] for blk in pool.table[b][:-(-c // 16)]])))
+        for b, c in enumerate(ctx)])
+    tol = (2.0 ** -11 + 2.0 ** -12) * mag + \
+        2.0 ** -24 * vmax[:, None, None] * 300
+    assert (np.abs(got - ref) <= tol).all()
+    assert torch.equal(out, out32.to(dtype)) or dtype == HF
+
+
+def test_decode_nan_reaches_its_own_row_only(pkv):
+    ctx = [40, 40]
+    pool = Pool(1, 64, 16, ctx, seed=2)
+    pool.kc[int(pool.table[0, 1]), 0, 3, 5] = torch.tensor(
+        float("nan"), device="cuda").to(E4M3)
+    q = torch.randn(2, 4, 64, device="cuda").to(BF)
+    out32, _ = decode(pkv, pool, q, 0.125)
+    assert torch.isnan(out32[0]).all() and torch.isfinite(out32[1]).all()
+
+
+def test_decode_device_errors(pkv):
+    from paged_kv_cache_383_b200 import _lib
+    ctx = [40, 90, 20]
+    for parts in (16, 64):
+        for edit in ("id", "len", "negative"):
+            pool = Pool(2, 64, 16, ctx, seed=6)
+            q = torch.randn(3, 4, 64, device="cuda").to(HF)
+            ref, mag = reference(pool, q, [(b, c - 1) for b, c in
+                                           enumerate(ctx)], 0.125)
+            if edit == "id":
+                pool.dev[0][1, 2] = pool.n
+            else:
+                pool.dev[1][1] = 97 if edit == "len" else -1
+            out = torch.zeros(3, 4, 64, device="cuda")
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            pkv.pa_decode_q8(out, q, *pool.cache, *pool.dev, 0.125,
+                             partition_size=parts, dev_err=err)
+            torch.cuda.synchronize()
+            assert err.item() == _lib.PA_ERR_DEVICE_OOB
+            for r in (0, 2):
+                assert (np.abs(to64(out)[r] - ref[r]) <=
+                        2.0 ** -14 * mag[r]).all()
+
+
+def test_copy_and_swap(pkv):
+    """Codes and scales move exactly, within a pool and to pinned host memory
+    and back; bad pairs are flagged and skipped."""
+    from paged_kv_cache_383_b200 import _lib
+    for hkv, d, bs in ((8, 128, 16), (1, 64, 32), (3, 64, 16)):
+        pool = Pool(hkv, d, bs, [200, 300], seed=4)
+        k0, v0, ks0, vs0 = (t.clone() for t in pool.cache)
+        pairs = torch.tensor([[0, 5], [1, 6], [0, 7], [99999, 2], [3, -1]],
+                             dtype=torch.int32, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pkv.pa_copy_blocks_q8(*pool.cache, pairs, dev_err=err)
+        torch.cuda.synchronize()
+        assert err.item() == _lib.PA_ERR_DEVICE_OOB
+        for t, t0 in zip(pool.cache, (k0, v0, ks0, vs0)):
+            want = t0.clone().view(torch.uint8)
+            for s, e in ((0, 5), (1, 6), (0, 7)):
+                want[e] = t0.view(torch.uint8)[s]
+            assert torch.equal(t.view(torch.uint8), want)
+        host = [torch.zeros((4,) + t.shape[1:], dtype=torch.uint8 if
+                            t.dtype == E4M3 else t.dtype).pin_memory()
+                for t in pool.cache]
+        host = [h.view(E4M3) if h.dtype == torch.uint8 else h for h in host]
+        out = torch.tensor([[7, 0], [2, 3]], dtype=torch.int32, device="cuda")
+        pkv.pa_swap_blocks_q8(*host, *pool.cache, out)
+        back = torch.tensor([[0, 8], [3, 9]], dtype=torch.int32,
+                            device="cuda")
+        pkv.pa_swap_blocks_q8(*pool.cache, *host, back)
+        torch.cuda.synchronize()
+        for t, h in zip(pool.cache, host):
+            u = t.view(torch.uint8)
+            assert torch.equal(u[8], u[7]) and torch.equal(u[9], u[2])
+            assert torch.equal(h.view(torch.uint8)[0], u[7].cpu())
+    with pytest.raises(ValueError):
+        pkv.pa_copy_blocks_q8(pool.kc, pool.vc, pool.ks.cpu(), pool.vs, pairs)
+    with pytest.raises(TypeError):
+        pkv.pa_copy_blocks_q8(pool.kc.view(torch.uint8),
+                              pool.vc.view(torch.uint8), pool.ks, pool.vs,
+                              pairs)
+
+
+def test_python_refusals_on_device(pkv):
+    pool = Pool(2, 64, 16, [20, 30], seed=1)
+    q = torch.zeros(2, 4, 64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="current device"):
+        pkv.pa_decode_q8(q.cpu(), q, *pool.cache, *pool.dev, 1.0)
+    with pytest.raises(TypeError):
+        pkv.pa_decode_q8(q, q, pool.kc.view(torch.uint8), *pool.cache[1:],
+                         *pool.dev, 1.0)
+    with pytest.raises(ValueError, match="contiguous"):
+        pkv.pa_decode_q8(q, q, *pool.cache, pool.dev[0].t().contiguous().t(),
+                         pool.dev[1], 1.0)
+    with pytest.raises(ValueError, match="k_scales"):
+        pkv.pa_decode_q8(q, q, pool.kc, pool.vc, pool.ks[:, :1], pool.vs,
+                         *pool.dev, 1.0)
+    with pytest.raises(pkv.PagedKVError):
+        pkv.pa_decode_q8(q, q, *pool.cache, *pool.dev, 1.0,
+                         workspace=torch.empty(
+                             1, dtype=torch.uint8, device="cuda"))
+
+
+def test_decode_on_another_stream(pkv):
+    """Without a workspace, on a stream other than the current one, while the
+    current stream allocates and writes."""
+    pool = Pool(8, 128, 16, [1500] * 8, seed=5)
+    q = torch.randn(8, 64, 128, device="cuda").to(BF)
+    want, _ = decode(pkv, pool, q, 0.09, partition_size=64)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for stream in (s, s.cuda_stream):
+        for _ in range(10):
+            out = torch.empty(q.shape, device="cuda")
+            pkv.pa_decode_q8(out, q, *pool.cache, *pool.dev, 0.09,
+                             partition_size=64, stream=stream)
+            outs.append(out)
+            torch.full((1 << 22,), float("nan"), device="cuda")
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+
+
+def test_decode_workload(pkv):
+    """The batch mix's lengths at a reduced batch, default options."""
+    w = wl.WORKLOADS["llama3_70b_gqa8"].scaled(num_seqs=12, cap=3000)
+    ctx = wl.draw_lengths(w, np.random.default_rng(1)).tolist()
+    pool = Pool(8, 128, 16, ctx, seed=7, spread=0.5)
+    q = torch.randn(12, 64, 128, device="cuda").to(BF)
+    out32, out = decode(pkv, pool, q, 128 ** -0.5,
+                        max_context_len=int(max(ctx)))
+    ref, mag = reference(pool, q, [(b, c - 1) for b, c in enumerate(ctx)],
+                         128 ** -0.5)
+    check(out32, out, ref, mag, BF)
