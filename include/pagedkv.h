@@ -531,6 +531,19 @@ pa_status pa_decode_q8(void* out, const void* q, const void* k_cache,
                        size_t workspace_bytes, int32_t* dev_err,
                        void* stream);
 
+/* pa_prefill over the 8-bit cache: the same descriptor (dtype is that of q
+ * and out; kernel and pv are checked but change nothing: the weights are
+ * fp16, which needs no residual), workspace (pa_prefill_workspace_bytes),
+ * launches, checks and errors.  Any scale sign; sizes as pa_prefill. */
+pa_status pa_prefill_q8(void* out, const void* q, const void* k_cache,
+                        const void* v_cache, const float* k_scales,
+                        const float* v_scales, const int32_t* block_tables,
+                        const int32_t* context_lens,
+                        const int32_t* query_start, float scale,
+                        const pa_prefill_desc* desc, void* workspace,
+                        size_t workspace_bytes, int32_t* dev_err,
+                        void* stream);
+
 /* pa_copy_blocks and pa_swap_blocks for the 8-bit cache: codes and scales of
  * whole blocks.  Pairs, pools and errors as there; head_dim a multiple of
  * 16. */

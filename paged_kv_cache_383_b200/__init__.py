@@ -34,6 +34,7 @@ __all__ = [
     "pa_cache_write",
     "pa_copy_blocks",
     "pa_append", "pa_append_q8", "pa_rope_freqs", "pa_decode_q8",
+    "pa_prefill_q8",
     "pa_copy_blocks_q8", "pa_swap_blocks_q8",
     "pa_pool_blocks_q8",
     "pa_decode_workspace_bytes", "pa_decode_partition_size", "make_desc",
@@ -628,6 +629,34 @@ def pa_decode_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
         *p[:8], scale, ctypes.byref(desc), p[8],
         workspace.numel() * workspace.element_size(), p[9], _stream(stream))
     _lib.check(st, "pa_decode_q8")
+    return out
+
+
+def pa_prefill_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                  context_lens, query_start, scale: float, *, max_q_len: int,
+                  max_context_len: int = 0, workspace=None, dev_err=None,
+                  stream=None):
+    """``pa_prefill`` over the 8-bit cache.  ``workspace`` (a uint8 CUDA
+    tensor of ``pa_prefill_workspace_bytes`` bytes) is allocated per call
+    when not given.  Returns ``out``."""
+    import torch
+    lib = _lib.load()
+    if query_start.shape != (block_tables.shape[0] + 1,):
+        raise ValueError("query_start must be [num_seqs + 1]")
+    desc = _prefill_desc(q, k_cache, block_tables, max_q_len,
+                         max_context_len)
+    _out_mode(desc, out, q.dtype)
+    if workspace is None:
+        workspace = _workspace(
+            lib.pa_prefill_workspace_bytes(ctypes.byref(desc)), q.device,
+            stream)
+    p = _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
+                        block_tables, context_lens, workspace, dev_err)
+    qs, = _on_current((query_start, "query_start", torch.int32))
+    st = lib.pa_prefill_q8(
+        *p[:8], qs, scale, ctypes.byref(desc), p[8],
+        workspace.numel() * workspace.element_size(), p[9], _stream(stream))
+    _lib.check(st, "pa_prefill_q8")
     return out
 
 

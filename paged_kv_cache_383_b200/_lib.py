@@ -160,6 +160,9 @@ SIGNATURES = {
     "pa_decode_q8": (_st, [_vp] * 8 + [ctypes.c_float,
                                        ctypes.POINTER(pa_decode_desc), _vp,
                                        ctypes.c_size_t, _vp, _vp]),
+    "pa_prefill_q8": (_st, [_vp] * 9 + [ctypes.c_float,
+                                        ctypes.POINTER(pa_prefill_desc), _vp,
+                                        ctypes.c_size_t, _vp, _vp]),
     "pa_copy_blocks_q8": (_st, [_vp] * 5 + [_int] * 5 + [_vp, _vp]),
     "pa_swap_blocks_q8": (_st, [_vp] * 9 + [_int] * 6 + [_vp, _vp]),
     "pa_pool_blocks_q8": (_i64, [ctypes.c_uint64, _int, _int, _int, _int]),

@@ -22,7 +22,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["status.cpp", "block_manager.cpp", "append.cu", "cache_ops.cu",
            "cache_ops_q8.cu", "decode.cu", "decode_q8.cu", "prefill.cu",
-           "probe.cu", "swap.cu"]
+           "prefill_q8.cu", "probe.cu", "swap.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # No --split-compile: splitting a translation unit's device code into
 # partitions compiled in parallel made the generated code differ from build to

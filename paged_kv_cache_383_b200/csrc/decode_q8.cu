@@ -27,8 +27,8 @@
 //  * Weights w = p vs 2^(10-E) are rounded to fp16 for the second product.
 //    E follows the exponent of the largest vs met so far (o is rescaled when
 //    it grows by more than 3), so w stays below 2^14 and small weights stay
-//    normal down to 2^-24.  The rounding is 2^-12 of a weight: below bf16's
-//    2^-9 of the output.  With fp16 outputs it would show, so there the
+//    normal down to 2^-24.  The rounding is 2^-11 of a weight, an eighth of a
+//    bf16 output's own 2^-8.  With fp16 outputs it would show, so there the
 //    weight's residual is a second MMA operand, as in the 16-bit kernel.
 //
 // The split of the work, the ring of TMA pages (swizzled 128 bytes wide at

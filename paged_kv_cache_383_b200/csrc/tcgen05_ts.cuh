@@ -1,5 +1,6 @@
-// tcgen05 helpers used only by the prefill kernel: the MMA whose A operand
-// sits in tensor memory, and 32- and 16-column stores of 32-bit words.
+// tcgen05 helpers used only by the prefill kernels: the MMA whose A operand
+// sits in tensor memory, 32- and 16-column stores and 16-column loads of
+// 32-bit words.
 #pragma once
 
 #include <cstdint>
@@ -48,6 +49,19 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr,
       "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
       "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
       : "memory");
+}
+
+// 32 lanes x 16 columns of 32-bit words to registers (this thread's lane).
+__device__ __forceinline__ void tmem_ld16u(uint32_t taddr,
+                                           uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]),
+        "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+        "=r"(v[15])
+      : "r"(taddr));
 }
 
 }  // namespace dev

@@ -113,6 +113,42 @@ def test_decode_q8_rejects(pkv):
     assert b"pa_decode_q8" in lib.pa_last_error()
 
 
+def test_prefill_q8_rejects(pkv):
+    from paged_kv_cache_383_b200 import _lib
+    lib = _lib.load()
+
+    def call(ptrs=None, scale=1.0, ws=FAKE, wsb=1 << 20, **kw):
+        base = dict(num_seqs=2, num_q_heads=8, num_kv_heads=2, head_dim=128,
+                    block_size=16, max_blocks_per_seq=4, num_blocks=16,
+                    dtype=1, total_q=10, max_q_len=8)
+        base.update(kw)
+        d = _lib.pa_prefill_desc(**base)
+        return lib.pa_prefill_q8(*(ptrs or [FAKE] * 9), scale,
+                                 ctypes.byref(d), ws, wsb, None, None)
+    assert call(head_dim=96) == 2
+    assert call(block_size=64) == 2
+    assert call(num_q_heads=6) == 2
+    assert call(num_q_heads=7) == 1
+    assert call(dtype=2) == 1
+    assert call(kernel=2) == 1
+    assert call(pv=3) == 1
+    assert call(out_fp32=2) == 1
+    assert call(scale=math.inf) == 1
+    assert call(num_blocks=0) == 1
+    assert call(ws=None) == _lib.PA_ERR_WORKSPACE
+    assert call(wsb=16) == _lib.PA_ERR_WORKSPACE
+    assert call(total_q=0, ws=None) == 0
+    for i in range(9):
+        p = [FAKE] * 9
+        p[i] = None
+        assert call(p) == 1, i
+    for i in range(4):
+        p = [FAKE] * 9
+        p[i] = FAKE + 8
+        assert call(p) == 1, i
+    assert b"pa_prefill_q8" in lib.pa_last_error()
+
+
 def test_block_moves_q8_reject(pkv):
     from paged_kv_cache_383_b200 import _lib
     lib = _lib.load()

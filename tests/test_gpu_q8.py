@@ -2,9 +2,9 @@
 oracle on the values that the codes and scales stand for.
 
 Tolerance on the float32 output, per element: the weights enter the second
-product in fp16, each off by at most 2^-11 of itself (bf16 outputs; twice the
-half step 2^-12 for the normalisation by their exact sum), or with its
-residual by 2^-22 (fp16 outputs); scores and exponentials in fp32 move a weight
+product in fp16, each off by at most half a step, 2^-11 of itself (the sum
+that divides them is exact), or in the decode of fp16 outputs, with its
+residual, by 2^-22; scores and exponentials in fp32 move a weight
 by less than 2^-16 (arguments below 2^7 rounded at 2^-24, 128 products
 accumulated in fp32).  Both act on sum p |v|:
   |err| <= (2^-11 or 2^-22, + 2^-15) * sum_t p_t |v_t|  + tiny.
@@ -315,3 +315,228 @@ def test_decode_workload(pkv):
     ref, mag = reference(pool, q, [(b, c - 1) for b, c in enumerate(ctx)],
                          128 ** -0.5)
     check(out32, out, ref, mag, BF)
+
+
+def prefill(pkv, pool, q, start, scale, max_q_len, **kw):
+    qs = torch.from_numpy(np.asarray(start, dtype=np.int32)).cuda()
+    out32 = torch.full(q.shape, float("nan"), device="cuda")
+    out = torch.zeros_like(q)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for o in (out32, out):
+        pkv.pa_prefill_q8(o, q, *pool.cache, *pool.dev, qs, scale,
+                          max_q_len=max_q_len, dev_err=err, **kw)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    return out32, out
+
+
+def positions(ctx, new):
+    """(sequence, last visible position) of every query row."""
+    return [(b, L - n + i) for b, (L, n) in enumerate(zip(ctx, new))
+            for i in range(n)]
+
+
+def bound_prefill(pool, q, qpos, scale, mag):
+    """The error allowed to each element.
+
+    Relative to sum p |v|: 2^-11 for a weight's rounding (no residual here,
+    fp16 outputs too), 2^-15 as above, and the scores' own error where
+    products are large: a score sums D products in D / 16 steps of the tensor
+    core, each of which may drop a unit in the last place (2^-23) of a partial
+    sum of at most A = max_t sum_d |q_d K_td|; the weight moves by that as the
+    exponential's argument does, and the weights' sum by as much again:
+    2 |scale| A (D / 16) 2^-23.
+
+    Absolute: a weight 2^8 p vs / 2^E below fp16's normal range is off by up
+    to half its smallest step, 2^-25, whatever its size; times 2^(E - 8) and
+    the code, with 2^E at most the largest vs and the weights' sum at least 1:
+    2^-33 max vs sum_t |vcode_t|."""
+    kv, _ = pool.values()
+    codes, vs = np.abs(to64(pool.vc)), to64(pool.vs)
+    q = np.abs(to64(q))
+    hq, hkv, d, bs = q.shape[1], kv.shape[1], q.shape[2], kv.shape[2]
+    amp, low = np.zeros(q.shape[:2] + (1,)), np.zeros_like(q)
+    for r, (b, p) in enumerate(qpos):
+        used = pool.table[b][:-(-int(pool.ctx[b]) // bs)]
+        for h in range(hkv):
+            K = np.abs(oa.depage(kv, pool.table[b], p + 1, h, bs))
+            c = oa.depage(codes, pool.table[b], p + 1, h, bs).sum(0)
+            for g in range(h * hq // hkv, (h + 1) * hq // hkv):
+                amp[r, g] = (K @ q[r, g]).max()
+                low[r, g] = 2.0 ** -33 * vs[used, h].max() * c
+    rel = 2.0 ** -11 + 2.0 ** -15 + \
+        2 * abs(scale) * amp * (d / 16) * 2.0 ** -23
+    return rel * mag[:len(rel)] + low + 1e-30
+
+
+def check_prefill(out32, out, ref, tol, n):
+    got = to64(out32)[:n]
+    assert (np.abs(got - ref[:n]) <= tol).all(), \
+        float((np.abs(got - ref[:n]) / tol).max())
+    assert torch.equal(out[:n], out32.to(out.dtype)[:n])
+
+
+PREFILL = [
+    # dtype, hq, hkv, d, bs, ctx, new
+    (BF, 8, 8, 64, 16, [1], [1]),
+    (HF, 2, 2, 128, 16, [130, 64, 65], [130, 64, 1]),
+    (BF, 16, 2, 128, 16, [17, 200, 0, 63], [17, 3, 0, 63]),
+    (HF, 8, 2, 128, 32, [300, 33, 95], [33, 33, 5]),
+    (BF, 4, 2, 64, 32, [257, 90], [200, 1]),
+    (HF, 8, 1, 64, 16, [100, 128, 31], [40, 128, 0]),
+    (BF, 64, 8, 128, 16, [400, 1000], [4, 5]),
+    (BF, 32, 8, 128, 32, [640], [97]),
+    (HF, 1, 1, 128, 16, [500], [500]),
+]
+
+
+@pytest.mark.parametrize("case", PREFILL,
+                         ids=lambda c: f"{c[1]}x{c[2]}x{c[3]}-{c[4]}")
+@pytest.mark.parametrize("pow2", [True, False])
+def test_prefill(pkv, case, pow2):
+    dtype, hq, hkv, d, bs, ctx, new = case
+    pool = Pool(hkv, d, bs, ctx, seed=len(ctx) + 20, pow2=pow2)
+    n = sum(new)
+    start = np.concatenate([[0], np.cumsum(new)])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(n + 2, hq, d, generator=g, device="cuda").to(dtype)
+    scale = d ** -0.5
+    out32, out = prefill(pkv, pool, q, start, scale, max(new))
+    ref, mag = reference(pool, q, positions(ctx, new), scale)
+    tol = bound_prefill(pool, q[:n], positions(ctx, new), scale, mag)
+    check_prefill(out32, out, ref, tol, n)
+    assert torch.isnan(out32[n:]).all()  # rows behind the last sequence
+    assert (out[n:] == 0).all()
+
+
+def test_prefill_many_items(pkv):
+    """More work items than CTAs, of very unlike lengths."""
+    rng = np.random.default_rng(5)
+    ctx = rng.integers(1, 500, size=40).tolist()
+    new = [int(rng.integers(0, c + 1)) for c in ctx]
+    new[3] = 0
+    pool = Pool(8, 64, 16, ctx, seed=40)
+    start = np.concatenate([[0], np.cumsum(new)])
+    q = torch.randn(int(start[-1]), 16, 64, device="cuda").to(BF)
+    out32, out = prefill(pkv, pool, q, start, 0.125, max(new))
+    rows = rng.choice(len(q), 60, replace=False)
+    pos = positions(ctx, new)
+    some = q[torch.from_numpy(rows).cuda()], [pos[r] for r in rows], 0.125
+    ref, mag = reference(pool, *some)
+    got = to64(out32)[rows]
+    assert (np.abs(got - ref) <= bound_prefill(pool, *some, mag)).all()
+    assert torch.equal(out, out32.to(BF))
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 3.0])
+def test_prefill_scales_and_ranges(pkv, scale):
+    """Negative, zero and steep softmax scales; block scales that span 60
+    binades, zeros among them; queries of unlike size."""
+    ctx, new = [300, 77], [150, 9]
+    pool = Pool(2, 128, 16, ctx, seed=9)
+    e = torch.arange(pool.n, device="cuda") * 37 % 61 - 30
+    ok = ~torch.isnan(pool.vs)
+    pool.vs.copy_(torch.where(
+        ok, torch.exp2(e.float())[:, None].expand(pool.n, 2), pool.vs))
+    for c, s, b in ((pool.vc, pool.vs, pool.table[0, 3]),
+                    (pool.kc, pool.ks, pool.table[0, 5])):
+        c[int(b)] = torch.zeros_like(c[int(b)].float()).to(E4M3)
+        s[int(b)] = 0.0
+    q = torch.randn(159, 16, 128, device="cuda")
+    q[:, 3] *= 8
+    q[:, 4] *= 2.0 ** -13
+    q[:, 5] = 0
+    q = q.to(BF)
+    start = [0, 150, 159]
+    out32, out = prefill(pkv, pool, q, start, scale, 150)
+    ref, mag = reference(pool, q, positions(ctx, new), scale)
+    # and arguments up to 2^10, rounded at 2^-24: 2^-13 on a weight, twice
+    tol = bound_prefill(pool, q, positions(ctx, new), scale, mag) + \
+        2.0 ** -12 * mag
+    assert (np.abs(to64(out32) - ref) <= tol).all()
+
+
+def test_prefill_nan_reaches_its_own_rows_only(pkv):
+    ctx, new = [70, 70], [10, 10]
+    pool = Pool(1, 64, 16, ctx, seed=2)
+    nan = torch.tensor(float("nan"), device="cuda").to(E4M3)
+    pool.kc[int(pool.table[0, 4]), 0, 1, 5] = nan   # position 65
+    q = torch.randn(20, 4, 64, device="cuda").to(BF)
+    out32, _ = prefill(pkv, pool, q, [0, 10, 20], 0.125, 10)
+    assert torch.isfinite(out32[:5]).all()      # positions 60 .. 64
+    assert torch.isnan(out32[5:10]).all()
+    assert torch.isfinite(out32[10:]).all()
+
+
+def test_prefill_device_errors(pkv):
+    from paged_kv_cache_383_b200 import _lib
+    ctx, new = [40, 90, 20], [4, 70, 20]
+    start = [0, 4, 74, 94]
+    for edit in ("id", "len", "short", "max_q_len"):
+        pool = Pool(2, 64, 16, ctx, seed=6)
+        q = torch.randn(94, 4, 64, device="cuda").to(HF)
+        ref, mag = reference(pool, q, positions(ctx, new), 0.125)
+        tol = bound_prefill(pool, q, positions(ctx, new), 0.125, mag)
+        m = 70
+        if edit == "id":
+            pool.dev[0][1, 2] = -3
+        elif edit == "max_q_len":
+            m = 60
+        else:
+            pool.dev[1][1] = 97 if edit == "len" else 60
+        out = torch.zeros(94, 4, 64, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pkv.pa_prefill_q8(
+            out, q, *pool.cache, *pool.dev,
+            torch.tensor(start, dtype=torch.int32, device="cuda"), 0.125,
+            max_q_len=m, dev_err=err)
+        torch.cuda.synchronize()
+        assert err.item() == _lib.PA_ERR_DEVICE_OOB
+        for r in list(range(4)) + list(range(74, 94)):
+            assert (np.abs(to64(out)[r] - ref[r]) <= tol[r]).all()
+
+
+def test_attention_in_a_graph(pkv):
+    """Decode and prefill captured together, replayed after the cache, the
+    lengths and the queries changed."""
+    pool = Pool(2, 128, 16, [100, 40], seed=3)
+    q1 = torch.randn(2, 8, 128, device="cuda").to(BF)
+    q2 = torch.randn(10, 8, 128, device="cuda").to(BF)
+    qs = torch.tensor([0, 7, 10], dtype=torch.int32, device="cuda")
+    o = [torch.zeros_like(q1), torch.zeros_like(q2)]
+    ws = [torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+          for _ in "12"]
+
+    def step(out):
+        pkv.pa_decode_q8(out[0], q1, *pool.cache, *pool.dev, 0.09,
+                         max_context_len=112, workspace=ws[0])
+        pkv.pa_prefill_q8(out[1], q2, *pool.cache, *pool.dev, qs, 0.09,
+                          max_q_len=7, workspace=ws[1])
+    step(o)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(o)
+    for n in (100, 90, 65):
+        pool.dev[1][0] = n
+        q1.copy_(torch.randn_like(q1))
+        q2.copy_(torch.randn_like(q2))
+        pool.vs *= 2
+        graph.replay()
+        want = [torch.zeros_like(q1), torch.zeros_like(q2)]
+        step(want)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_prefill_of_one_token_is_decode(pkv):
+    """One new token per sequence: the two kernels agree to their rounding."""
+    ctx = [5, 100, 777, 64]
+    pool = Pool(4, 128, 32, ctx, seed=11)
+    q = torch.randn(4, 16, 128, device="cuda").to(HF)
+    a, _ = decode(pkv, pool, q, 0.09)
+    b, _ = prefill(pkv, pool, q, [0, 1, 2, 3, 4], 0.09, 1)
+    pos = [(i, c - 1) for i, c in enumerate(ctx)]
+    _, mag = reference(pool, q, pos, 0.09)
+    tol = 2 * bound_prefill(pool, q, pos, 0.09, mag)  # one's, the other's
+    assert (np.abs(to64(a) - to64(b)) <= tol).all()
