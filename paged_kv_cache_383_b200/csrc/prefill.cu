@@ -1255,8 +1255,8 @@ extern "C" pa_status pa_prefill(void* out, const void* q, const void* k_cache,
   a.pv_split = d->pv;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const pa_status planned = pagedkv::launch_plan(
-      "pa_prefill", d, context_lens, query_start, max_ctx, workspace, dev_err,
-      s);
+      "pa_prefill", d, context_lens, query_start, max_ctx,
+      pagedkv::tile_tokens(d), workspace, dev_err, s);
   if (planned != PA_OK) return planned;
   if (rq == 8)
     return d->dtype == PA_BF16

@@ -156,11 +156,14 @@ __global__ void __launch_bounds__(kOrderThreads)
 int tile_tokens(const pa_prefill_desc* d) {
   return kRows / (d->num_q_heads / d->num_kv_heads);
 }
-int64_t tile_cap(const pa_prefill_desc* d) {
-  const int tok = tile_tokens(d);
+int64_t tile_cap(const pa_prefill_desc* d, int tok) {
   return std::min(static_cast<int64_t>(d->total_q) / tok + d->num_seqs,
                   static_cast<int64_t>(d->num_seqs) *
                       ((static_cast<int64_t>(d->max_q_len) + tok - 1) / tok));
+}
+
+int64_t tile_cap(const pa_prefill_desc* d) {
+  return tile_cap(d, tile_tokens(d));
 }
 
 // The sequence order (num_seqs int32, rounded up to 16 bytes), the work
@@ -255,10 +258,12 @@ pa_status check_prefill(const char* fn, const void* out, const void* q,
   return PA_OK;
 }
 
+// The map lists tiles of `tok` tokens (at least tile_tokens(d), whose map the
+// workspace holds).
 pa_status launch_plan(const char* fn, const pa_prefill_desc* d,
                       const int32_t* context_lens, const int32_t* query_start,
-                      int max_ctx, void* workspace, int32_t* dev_err,
-                      cudaStream_t s) {
+                      int max_ctx, int tok, void* workspace,
+                      int32_t* dev_err, cudaStream_t s) {
   int2* tiles = tile_map(d, workspace);
   int* counter = work_counter(d, workspace);
   cudaLaunchConfig_t pcfg = {};
@@ -273,7 +278,7 @@ pa_status launch_plan(const char* fn, const pa_prefill_desc* d,
   cudaError_t oe = cudaLaunchKernelEx(
       &pcfg, prefill_plan_kernel, context_lens, query_start,
       d->num_seqs, d->total_q, d->max_q_len, order_shift(max_ctx),
-      tile_tokens(d), static_cast<int>(tile_cap(d)),
+      tok, static_cast<int>(tile_cap(d, tok)),
       static_cast<int32_t*>(workspace), tiles, counter, dev_err);
   count_launch();
   if (oe == cudaSuccess) oe = cudaGetLastError();

@@ -55,19 +55,25 @@ namespace pagedkv {
 namespace {
 
 constexpr int kKeys = 64;        // keys per K/V tile
+constexpr int kPair = 2;         // query tiles (128 rows each) per work item
+constexpr int kStages = 4;       // fp16 K tiles, and V tiles
 constexpr int kRaw = 4;          // tiles of codes in flight (K and V in turn)
-constexpr int kScaleSlots = 8;   // tiles whose scales are staged
-// Warps 0..3 softmax, 4..7 converters, 8 pages and scales, 9 MMA (10 and 11
-// only complete its warpgroup).  Registers: 80 a thread at launch, shared out
-// anew between the warpgroups; kept at 80 x 3 in sum (an increase waits for
-// registers that the others gave up).
-constexpr int kThreads = 384;
-constexpr int kConvThreads = 128;
-constexpr int kLaunchRegs = 80;
-constexpr int kSoftmaxRegs = 176, kConvRegs = 24, kIssueRegs = 40;
-static_assert(kSoftmaxRegs + kConvRegs + kIssueRegs == 3 * kLaunchRegs,
+constexpr int kScaleSlots = 16;  // tiles whose scales are staged
+// Warps 0..3 and 4..7: softmax of query tile 0 and 1; 8..11 converters; 12
+// pages and scales; 13 and 14 MMAs of query tile 0 and 1.
+constexpr int kConvWarp = 8, kPageWarp = 12, kMmaWarp = 13;
+constexpr int kThreads = 16 * 32;  // whole warpgroups; warp 15 has no work
+// Registers: 128 a thread at launch, shared out anew between the warpgroups
+// (a softmax thread holds 64 scores).  The sum must not exceed the launch's:
+// an increase waits for registers that the others gave up.
+constexpr int kLaunchRegs = 128;
+constexpr int kSoftmaxRegs = 192, kConvRegs = 48, kIssueRegs = 80;
+static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs == 4 * kLaunchRegs,
               "more registers than the block was launched with");
-constexpr int kTmemCols = 256;   // S [0, 64), P [64, 96), O [128, 128 + D)
+// Tensor memory columns, for each query tile: S 64, P 32, the last 64 dims of
+// q 32, O head_dim (up to 128).
+constexpr int kTmemCols = 512;
+constexpr int kColS = 0, kColP = 128, kColQ = 192, kColO = 256;
 // fp16 weights stay below 2^15: a maximum may grow by 2^kRescaleLog2 and a
 // block's vs exceed 2^E by less than 2^(kVsSlack + 1) before O is rescaled.
 constexpr float kRescaleLog2 = 4.f;
@@ -99,26 +105,29 @@ struct PrefillQ8Args {
   int num_items;
 };
 
-// q_full, raw_full[], raw_empty[], k_full, k_empty, v_full, v_empty, s_full,
-// s_free, p_full, o_ready, done, q_empty, item_full[2], item_empty[2].
-constexpr int kNumBars = 1 + 2 * kRaw + 4 + 4 + 2 + 4;
+// raw_full[], raw_empty[], k_full[], k_empty[], v_full[], v_empty[]; for each
+// of the pair q_full, q_empty, s_full, s_free, p_full, o_done; done; item_full[2],
+// item_empty[2].
+constexpr int kNumBars = 2 * kRaw + 4 * kStages + 6 * kPair + 1 + 4;
 constexpr int kItemWords = 8;
 
 template <int D>
 struct LayoutQ8 {
   static constexpr int kHalves = D / 64;
-  static constexpr int kHalfQ = kRows * 128;
+  // q's last 64 dims are in tensor memory, those before in shared memory.
+  static constexpr int kQTile = (kHalves - 1) * kRows * 128;
   static constexpr int kTile = kHalves * kTileHalf;  // fp16 K or V tile
   static constexpr int kRawTile = kKeys * D;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kHalves * kHalfQ;
-  static constexpr int kOffV = kOffK + kTile;
-  static constexpr int kOffRaw = kOffV + kTile;
+  static constexpr int kOffK = kOffQ + kPair * kQTile;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffRaw = kOffV + kStages * kTile;
   static constexpr int kOffScales = kOffRaw + kRaw * kRawTile;
   static constexpr int kOffBars = kOffScales + kScaleSlots * 32;
   static constexpr size_t kSmemBytes =
       1024 + kOffBars + kNumBars * 8 + 16 + 2 * kItemWords * 4;
 };
+static_assert(LayoutQ8<128>::kSmemBytes <= 232448, "shared memory of an SM");
 
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -127,6 +136,30 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+constexpr uint32_t kSuspendNs = 20000;
+
+// dev::mbar_wait with a suspend-time hint: a waiting thread sleeps in the
+// barrier instead of polling it, which leaves the issue slots to the others.
+__device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  if (try_wait_hint(bar, parity)) return true;
+  const uint64_t t0 = dev::globaltimer();
+  while (!try_wait_hint(bar, parity)) {
+    if (dev::globaltimer() - t0 > dev::kWaitLimitNs) return false;
+  }
+  return true;
 }
 
 // `bytes` contiguous bytes global -> shared, counted on `bar`.
@@ -140,35 +173,37 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
 }
 
 template <typename T, int BS, int G, int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     prefill_q8_kernel(const PrefillQ8Args a) {
   using Lay = LayoutQ8<D>;
   using M = dev::Mma<__half>;
-  constexpr int kTok = kRows / G;   // new tokens per tile
-  constexpr int kNB = kKeys / BS;   // blocks (pages) per tile
+  constexpr int kHalves = Lay::kHalves;
+  constexpr int kTok = kRows / G;           // new tokens per query tile
+  constexpr int kItemTok = kPair * kTok;    // and per work item
+  constexpr int kNB = kKeys / BS;           // blocks (pages) per K/V tile
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem =
       smem_dyn + ((1024u - (dev::smem_u32(smem_dyn) & 1023u)) & 1023u);
   const uint32_t base = dev::smem_u32(smem);
-  const uint32_t q_s = base + Lay::kOffQ;
-  const uint32_t k_s = base + Lay::kOffK;
-  const uint32_t v_s = base + Lay::kOffV;
   float* scale_s = reinterpret_cast<float*>(smem + Lay::kOffScales);
   const uint32_t bars = base + Lay::kOffBars;
-  const uint32_t q_full = bars;
-  const uint32_t raw_full0 = q_full + 8;
+  const uint32_t raw_full0 = bars;
   const uint32_t raw_empty0 = raw_full0 + 8 * kRaw;
-  const uint32_t k_full = raw_empty0 + 8 * kRaw;
-  const uint32_t k_empty = k_full + 8;
-  const uint32_t v_full = k_empty + 8;
-  const uint32_t v_empty = v_full + 8;
-  const uint32_t s_full = v_empty + 8;
-  const uint32_t s_free = s_full + 8;
-  const uint32_t p_full = s_free + 8;
-  const uint32_t o_ready = p_full + 8;
-  const uint32_t done = o_ready + 8;
-  const uint32_t q_empty = done + 8;
-  const uint32_t item_full0 = q_empty + 8;
+  const uint32_t k_full0 = raw_empty0 + 8 * kRaw;
+  const uint32_t k_empty0 = k_full0 + 8 * kStages;
+  const uint32_t v_full0 = k_empty0 + 8 * kStages;
+  const uint32_t v_empty0 = v_full0 + 8 * kStages;
+  // For query tile x of the pair: its q is in place / the item's S MMAs are
+  // done with it; S(t) is in tensor memory / in the softmax warps' registers;
+  // P(t) is in tensor memory; P(t).V is done (O is current, P's buffer free).
+  const uint32_t q_full0 = v_empty0 + 8 * kStages;
+  const uint32_t q_empty0 = q_full0 + 8 * kPair;
+  const uint32_t s_full0 = q_empty0 + 8 * kPair;
+  const uint32_t s_free0 = s_full0 + 8 * kPair;
+  const uint32_t p_full0 = s_free0 + 8 * kPair;
+  const uint32_t o_done0 = p_full0 + 8 * kPair;
+  const uint32_t done = o_done0 + 8 * kPair;
+  const uint32_t item_full0 = done + 8;
   const uint32_t item_empty0 = item_full0 + 16;
   uint32_t* tmem_slot =
       reinterpret_cast<uint32_t*>(smem + Lay::kOffBars + kNumBars * 8);
@@ -177,28 +212,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   dev::pdl_trigger();
   if (tid == 0) {
-    dev::mbar_init(q_full, 4);
     for (int s = 0; s < kRaw; ++s) {
       dev::mbar_init(raw_full0 + 8 * s, 1);
       dev::mbar_init(raw_empty0 + 8 * s, 4);
     }
-    dev::mbar_init(k_full, 4);
-    dev::mbar_init(k_empty, 1);
-    dev::mbar_init(v_full, 4);
-    dev::mbar_init(v_empty, 1);
-    dev::mbar_init(s_full, 1);
-    dev::mbar_init(s_free, 4);
-    dev::mbar_init(p_full, 4);
-    dev::mbar_init(o_ready, 1);
-    dev::mbar_init(done, 4);
-    dev::mbar_init(q_empty, 1);
+    for (int s = 0; s < kStages; ++s) {
+      dev::mbar_init(k_full0 + 8 * s, 4);
+      dev::mbar_init(k_empty0 + 8 * s, 2);
+      dev::mbar_init(v_full0 + 8 * s, 4);
+      dev::mbar_init(v_empty0 + 8 * s, 2);
+    }
+    for (int x = 0; x < kPair; ++x) {
+      dev::mbar_init(q_full0 + 8 * x, 4);
+      dev::mbar_init(q_empty0 + 8 * x, 1);
+      dev::mbar_init(s_full0 + 8 * x, 1);
+      dev::mbar_init(s_free0 + 8 * x, 4);
+      dev::mbar_init(p_full0 + 8 * x, 4);
+      dev::mbar_init(o_done0 + 8 * x, 1);
+    }
+    dev::mbar_init(done, 8);
     for (int s = 0; s < 2; ++s) {
       dev::mbar_init(item_full0 + 8 * s, 1);
-      dev::mbar_init(item_empty0 + 8 * s, 9);
+      dev::mbar_init(item_empty0 + 8 * s, 14);
     }
     dev::fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     dev::tmem_alloc(dev::smem_u32(tmem_slot), kTmemCols);
     dev::tmem_relinquish();
   }
@@ -206,9 +245,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const uint32_t s_tmem = tbase;
-  const uint32_t p_tmem = tbase + kKeys;
-  const uint32_t o_tmem = tbase + 128;
   dev::pdl_wait();
 
   struct Item {
@@ -216,20 +252,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     int b, kvh, qt, L, q0, q_len;
   };
   constexpr int kWork = 0, kSkip = 1, kEnd = 2;
+  // What an item computes: for query tile x new tokens tok0[x] .. + n_q[x] - 1
+  // over n_tiles[x] tiles of keys (0: no such rows); tile 1 has the later
+  // tokens, so n_tiles[1] >= n_tiles[0] or 0.  kv_end: the keys it sees.
   struct Span {
-    int tok0, n_q, kv_end, n_tiles;
+    int tok0[kPair], n_q[kPair], n_tiles[kPair], kv_end, tiles;
   };
   auto span_of = [](const Item& it) {
     Span sp;
-    sp.tok0 = it.qt * kTok;
-    sp.n_q = min(kTok, it.q_len - sp.tok0);
-    sp.kv_end = it.L - it.q_len + sp.tok0 + sp.n_q;
-    sp.n_tiles = (sp.kv_end + kKeys - 1) / kKeys;
+    sp.kv_end = 0;
+#pragma unroll
+    for (int x = 0; x < kPair; ++x) {
+      sp.tok0[x] = it.qt * kItemTok + x * kTok;
+      sp.n_q[x] = max(0, min(kTok, it.q_len - sp.tok0[x]));
+      const int end = it.L - it.q_len + sp.tok0[x] + sp.n_q[x];
+      sp.n_tiles[x] = sp.n_q[x] > 0 ? (end + kKeys - 1) / kKeys : 0;
+      if (sp.n_q[x] > 0) sp.kv_end = end;
+    }
+    sp.tiles = max(sp.n_tiles[0], sp.n_tiles[1]);
     return sp;
   };
   auto read_item = [&](int n, Item& it) -> bool {
     const int slot = n & 1;
-    if (!dev::mbar_wait(item_full0 + 8 * slot, (n >> 1) & 1)) return false;
+    if (!wait_bar(item_full0 + 8 * slot, (n >> 1) & 1)) return false;
     const volatile int* d = item_s + kItemWords * slot;
     it.state = d[0];
     it.b = d[1];
@@ -240,7 +285,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     it.q_len = d[6];
     return true;
   };
-  // The same for a whole warp (the waits of collectives are warp-uniform).
+  // Waits of a whole warp, with a warp-uniform result (collectives follow).
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity));
+  };
   auto next_item = [&](int n, Item& it) -> bool {
     if (!__all_sync(0xffffffffu, read_item(n, it))) return false;
     __syncwarp();
@@ -248,18 +296,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     return true;
   };
 
-  if (warp >= 8) regs_dec<kIssueRegs>();
-  if (warp == 8) {
+  if (warp >= kPageWarp) regs_dec<kIssueRegs>();
+  if (warp == kPageWarp) {
     // ---------------- work items, pages and scales ----------------
     // Lane p looks after page p of each tile.
     const int p = lane;
     const bool mine = p < kNB;
     uint32_t u = 0;  // raw tiles of this CTA so far
-    uint32_t g = 0;  // tiles of this CTA's earlier items
+    uint32_t g = 0;  // K/V tiles of this CTA's earlier items
     bool ok = true;
-    auto warp_wait = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, dev::mbar_wait(bar, parity));
-    };
     auto acquire = [&]() -> bool {
       return u < kRaw ||
              warp_wait(raw_empty0 + 8 * (u % kRaw), ((u / kRaw) - 1) & 1);
@@ -298,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             it.L < 0 || it.L > a.max_blocks_per_seq * BS ||
             it.L > a.max_context_len || it.q_len < 0 || it.q_len > it.L ||
             it.q0 < 0 || it.q0 > a.total_q - it.q_len ||
-            it.qt * kTok >= it.q_len;
+            it.qt * kItemTok >= it.q_len;
         if (bad && lane == 0) dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
         it.state = bad ? kSkip : kWork;
       }
@@ -346,23 +391,24 @@ __global__ void __launch_bounds__(kThreads, 2)
       float2 sc = make_float2(1.f, 0.f), nsc = sc;
       if (mine) {
         nxt = fetch(0);
-        if (sp.n_tiles > 1) nn = fetch(1);
+        if (sp.tiles > 1) nn = fetch(1);
         nsc = fetch_scales(0, nxt);
       }
-      for (int t = 0; t <= sp.n_tiles; ++t) {
-        if (t < sp.n_tiles) {
+      for (int t = 0; t <= sp.tiles; ++t) {
+        if (t < sp.tiles) {
           cur = nxt;
           nxt = nn;
           sc = nsc;
-          if (mine && t + 2 < sp.n_tiles) nn = fetch(t + 2);
-          if (mine && t + 1 < sp.n_tiles) nsc = fetch_scales(t + 1, nxt);
+          if (mine && t + 2 < sp.tiles) nn = fetch(t + 2);
+          if (mine && t + 1 < sp.tiles) nsc = fetch_scales(t + 1, nxt);
           if (!acquire()) {
             ok = false;
             break;
           }
-          // A slot is written again kScaleSlots tiles on.  With kRaw tiles
-          // in flight the K tile it comes with is at most three ahead of the
-          // one whose S is next, so its old reader is long past.
+          // A slot is written again kScaleSlots tiles on.  K tile t is copied
+          // at most two tiles ahead of the one being converted, which is at
+          // most kStages ahead of the one whose S is next, at most two ahead
+          // of the one in the softmax: the slot's old readers are past it.
           if (mine) {
             float* to = scale_s + ((g + t) % kScaleSlots) * 8;
             to[p] = sc.x;
@@ -380,57 +426,88 @@ __global__ void __launch_bounds__(kThreads, 2)
         prv = cur;
       }
       if (bad_id) dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
-      g += sp.n_tiles;
+      g += sp.tiles;
     }
     if (!ok && lane == 0) dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
     return;
   }
 
-  if (warp >= 10) return;
-  if (warp == 9) {
-    // ---------------- MMA issuer ----------------
+  if (warp >= kMmaWarp + kPair) return;
+  if (warp >= kMmaWarp) {
+    // ---------------- MMA issuers, one per query tile ----------------
     if (lane == 0) {
+      const int x = warp - kMmaWarp;
       bool ok = true;
       constexpr uint32_t idesc_qk =
           dev::umma_idesc_f16(false, kRows, kKeys, false, false);
       constexpr uint32_t idesc_pv =
           dev::umma_idesc_f16(false, kRows, D, false, true);
-      auto issue_pv = [&](uint32_t t, bool first) -> bool {
-        if (!dev::mbar_wait(v_full, t & 1) || !dev::mbar_wait(p_full, t & 1))
-          return false;
-        dev::tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk) {
-          const uint64_t bd =
-              dev::sw128_desc(v_s + kk * 2048, kTileHalf, 1024);
-          dev::umma_f16_ts(o_tmem, p_tmem + kk * 8, bd, idesc_pv,
-                           (!first || kk > 0) ? 1u : 0u);
-        }
-        dev::umma_commit(o_ready);
-        dev::umma_commit(v_empty);
-        return true;
-      };
+      const uint32_t s_tmem = tbase + kColS + x * 64;
+      const uint32_t p_tmem = tbase + kColP + x * 32;
+      const uint32_t qt_tmem = tbase + kColQ + x * 32;
+      const uint32_t o_tmem = tbase + kColO + x * 128;
+      const uint32_t s_full = s_full0 + 8 * x, s_free = s_free0 + 8 * x;
+      const uint32_t p_full = p_full0 + 8 * x, o_done = o_done0 + 8 * x;
+      // Descriptors differ from these by an offset in their address field
+      // (16-byte units): one addition each.
+      const uint64_t qd =
+          dev::sw128_desc(base + Lay::kOffQ + x * Lay::kQTile, 16, 1024);
+      const uint64_t kd = dev::sw128_desc(base + Lay::kOffK, 16, 1024);
+      const uint64_t vd = dev::sw128_desc(base + Lay::kOffV, kTileHalf, 1024);
+      uint32_t g = 0;   // K/V tiles of this CTA's earlier items
+      uint32_t ts = 0;  // S tiles issued (query tile x)
+      int v = 0;        // items
+      // S(t) = Q K(t)^T: the dims whose q is in tensor memory need no read of
+      // the A operand from shared memory, which at 64 keys a tile is what
+      // bounds the other form.
       auto issue_s = [&](uint32_t t, bool last) -> bool {
-        if (!dev::mbar_wait(k_full, t & 1) ||
-            (t >= 1 && !dev::mbar_wait(s_free, (t - 1) & 1)))
+        const uint32_t s = t % kStages;
+        if (!wait_bar(k_full0 + 8 * s, (t / kStages) & 1) ||
+            (ts >= 1 && !wait_bar(s_free, (ts - 1) & 1)))
           return false;
         dev::tc_fence_after();
+        const uint64_t k = kd + s * (Lay::kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int h = kk >> 2, k4 = kk & 3;
-          const uint64_t ad =
-              dev::sw128_desc(q_s + h * Lay::kHalfQ + k4 * 32, 16, 1024);
-          const uint64_t bd =
-              dev::sw128_desc(k_s + h * kTileHalf + k4 * 32, 16, 1024);
-          dev::umma_f16(s_tmem, ad, bd, idesc_qk, kk > 0 ? 1u : 0u);
+          const uint64_t kb = k + ((h * kTileHalf + k4 * 32) >> 4);
+          if (h + 1 < kHalves)
+            dev::umma_f16(s_tmem, qd + ((h * kRows * 128 + k4 * 32) >> 4), kb,
+                          idesc_qk, kk > 0 ? 1u : 0u);
+          else
+            dev::umma_f16_ts(s_tmem, qt_tmem + k4 * 8, kb, idesc_qk,
+                             kk > 0 ? 1u : 0u);
         }
         dev::umma_commit(s_full);
-        dev::umma_commit(k_empty);
-        if (last) dev::umma_commit(q_empty);
+        dev::umma_commit(k_empty0 + 8 * s);
+        if (last) dev::umma_commit(q_empty0 + 8 * x);
+        ++ts;
         return true;
       };
-      uint32_t g = 0;
-      int v = 0;
+      // O (+)= P(t) V(t); p: P's phase.
+      auto issue_pv = [&](uint32_t t, uint32_t p, bool first) -> bool {
+        const uint32_t s = t % kStages;
+        if (!wait_bar(v_full0 + 8 * s, (t / kStages) & 1) ||
+            !wait_bar(p_full, p & 1))
+          return false;
+        dev::tc_fence_after();
+        const uint64_t vb = vd + s * (Lay::kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          dev::umma_f16_ts(o_tmem, p_tmem + kk * 8, vb + kk * (2048 >> 4),
+                           idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        dev::umma_commit(o_done);
+        dev::umma_commit(v_empty0 + 8 * s);
+        return true;
+      };
+      // A tile this query tile does not see (the other one does): only its
+      // share of the release, once the tile's phase has begun.
+      auto skip = [&](uint32_t t, uint32_t full0, uint32_t empty0) -> bool {
+        const uint32_t s = t % kStages;
+        if (!wait_bar(full0 + 8 * s, (t / kStages) & 1)) return false;
+        dev::mbar_arrive(empty0 + 8 * s);
+        return true;
+      };
       for (int n = 0; ok; ++n) {
         Item it;
         if (!read_item(n, it)) {
@@ -440,75 +517,89 @@ __global__ void __launch_bounds__(kThreads, 2)
         dev::mbar_arrive(item_empty0 + 8 * (n & 1));
         if (it.state == kEnd) break;
         if (it.state == kSkip) continue;
-        const int nt = span_of(it).n_tiles;
-        ok = dev::mbar_wait(q_full, v & 1) && issue_s(g, nt == 1);
-        for (int j = 0; ok && j < nt; ++j) {
-          if (j + 1 < nt) ok = issue_s(g + j + 1, j + 2 == nt);
-          if (ok) ok = issue_pv(g + j, j == 0);
+        const Span sp = span_of(it);
+        const int nt = x ? sp.n_tiles[1] : sp.n_tiles[0];
+        if (nt > 0) {
+          ok = wait_bar(q_full0 + 8 * x, v & 1) && issue_s(g, nt == 1);
+          ++v;
+        } else {
+          ok = skip(g, k_full0, k_empty0);
         }
-        g += nt;
-        ++v;
+        // S(j+1) goes ahead of P(j).V, which waits for the softmax.
+        for (int j = 0; ok && j < sp.tiles; ++j) {
+          if (j + 1 < nt)
+            ok = issue_s(g + j + 1, j + 2 == nt);
+          else if (j + 1 < sp.tiles)
+            ok = skip(g + j + 1, k_full0, k_empty0);
+          if (!ok) break;
+          if (j < nt)
+            ok = issue_pv(g + j, ts - (j + 1 < nt ? 2 : 1), j == 0);
+          else
+            ok = skip(g + j, v_full0, v_empty0);
+        }
+        g += sp.tiles;
       }
-      if (ok && g > 0) ok = dev::mbar_wait(o_ready, (g - 1) & 1);
       if (!ok) dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
-      if (!dev::mbar_wait(done, 0))
-        dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
+      // Tensor memory is released once the softmax warps are done with it;
+      // they have then seen their last P.V complete.
+      if (!wait_bar(done, 0)) dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
     }
     __syncwarp();
     dev::tc_fence_after();
-    dev::tmem_dealloc(tbase, kTmemCols);
+    if (warp == kMmaWarp) dev::tmem_dealloc(tbase, kTmemCols);
     return;
   }
 
-  if (warp >= 4) {
+  if (warp >= kConvWarp) {
     // ---------------- converters: codes -> fp16 tiles ----------------
     regs_dec<kConvRegs>();
-    const int ctid = tid - 4 * 32;
-    // This thread's 16-code chunk, in rows my_row, my_row + kRowStep, ...:
-    // two 16-byte chunks of fp16 in the swizzled tile (kRowStep is a multiple
-    // of 8, so their places in the row stay).  Threads of the second half of
-    // head_dim store their two in the opposite order: the eight lanes of a
-    // store phase then hit eight different bank groups.
-    constexpr int kChunks = D / 16;
-    constexpr int kRowStep = kConvThreads / kChunks;
-    const int my_row = ctid / kChunks;
-    const bool swap = (ctid % kChunks) >= 4;
-    const int my_dst = (swap ? kTileHalf : 0) + my_row * 128;
-    const int my_chunk = 2 * (ctid & 3);
-    const int my_e = (my_chunk ^ (my_row & 7)) << 4;
-    const int my_o = ((my_chunk + 1) ^ (my_row & 7)) << 4;
-    const int my_a = swap ? my_o : my_e, my_b = swap ? my_e : my_o;
+    const int ctid = tid - kConvWarp * 32;
+    // This thread's 16-code chunks: chunk cc of a 64-dim half, in rows row0,
+    // row0 + 32, ...; each becomes two 16-byte chunks of fp16.  Odd rows take
+    // the halves in the opposite order: the eight lanes of a load phase then
+    // read all 32 banks, and those of a store phase (four even, four odd
+    // rows' chunks) hit eight different swizzled places.
+    const int cc = ctid & 3, row0 = ctid >> 2;
+    const int flip = kHalves == 2 ? row0 & 1 : 0;
+    const int e0 = row0 * 128 + (((2 * cc) ^ (row0 & 7)) << 4);
+    const int e1 = row0 * 128 + (((2 * cc + 1) ^ (row0 & 7)) << 4);
+    constexpr int kPer = kKeys / 32 * kHalves;  // chunks per thread and tile
     uint32_t u = 0, g = 0;
     bool ok = true;
-    auto warp_wait = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, dev::mbar_wait(bar, parity));
-    };
-    // Raw tile u into the fp16 tile at offset `dst`, once `empty` says that
-    // tile t - 1 there was read; rows from `limit` on become zeros (a key
-    // past the context has weight 0, but 0 * NaN is NaN in the MMA).
-    auto convert = [&](int dst, uint32_t full, uint32_t empty, uint32_t t,
+    // Raw tile u into the fp16 tile at offset `dst`, the n-th to be put there,
+    // once `empty` says that the one before was read; rows from `limit` on
+    // become zeros (a key past the context has weight 0, but 0 * NaN is NaN
+    // in the MMA).
+    auto convert = [&](int dst, uint32_t full, uint32_t empty, uint32_t n,
                        int limit) -> bool {
       const uint32_t slot = u % kRaw;
       if (!warp_wait(raw_full0 + 8 * slot, (u / kRaw) & 1) ||
-          (t >= 1 && !warp_wait(empty, (t - 1) & 1)))
+          (n >= 1 && !warp_wait(empty, (n - 1) & 1)))
         return false;
       const uint8_t* raw = smem + Lay::kOffRaw + slot * Lay::kRawTile +
-                           ctid * 16;
-      uint8_t* d = smem + dst + my_dst;
-#pragma unroll
-      for (int i = 0; i < kKeys / kRowStep; ++i) {
-        uint4 w = *reinterpret_cast<const uint4*>(raw + i * kConvThreads * 16);
-        if (my_row + i * kRowStep >= limit) w = make_uint4(0u, 0u, 0u, 0u);
-        const uint4 lo = make_uint4(
+                           row0 * D + cc * 16;
+      uint8_t* d = smem + dst;
+      auto chunk = [&](int row_step, int half, bool zero) {
+        uint4 w = *reinterpret_cast<const uint4*>(raw + row_step * D +
+                                                  half * 64);
+        if (zero) w = make_uint4(0u, 0u, 0u, 0u);
+        uint8_t* to = d + half * kTileHalf + row_step * 128;
+        *reinterpret_cast<uint4*>(to + e0) = make_uint4(
             dev::e4m3x2_to_f16x2(w.x), dev::e4m3x2_to_f16x2_hi(w.x),
             dev::e4m3x2_to_f16x2(w.y), dev::e4m3x2_to_f16x2_hi(w.y));
-        const uint4 hi = make_uint4(
+        *reinterpret_cast<uint4*>(to + e1) = make_uint4(
             dev::e4m3x2_to_f16x2(w.z), dev::e4m3x2_to_f16x2_hi(w.z),
             dev::e4m3x2_to_f16x2(w.w), dev::e4m3x2_to_f16x2_hi(w.w));
-        *reinterpret_cast<uint4*>(d + i * kRowStep * 128 + my_a) =
-            swap ? hi : lo;
-        *reinterpret_cast<uint4*>(d + i * kRowStep * 128 + my_b) =
-            swap ? lo : hi;
+      };
+      if (limit >= kKeys) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          chunk(32 * (i / kHalves), (i % kHalves) ^ flip, false);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i)
+          chunk(32 * (i / kHalves), (i % kHalves) ^ flip,
+                row0 + 32 * (i / kHalves) >= limit);
       }
       dev::fence_proxy_async_smem();  // visible to the tensor cores
       __syncwarp();
@@ -525,14 +616,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok || it.state == kEnd) break;
       if (it.state == kSkip) continue;
       const Span sp = span_of(it);
-      for (int t = 0; ok && t <= sp.n_tiles; ++t) {
-        if (t < sp.n_tiles)
-          ok = convert(Lay::kOffK, k_full, k_empty, g + t, kKeys);
-        if (ok && t >= 1)
-          ok = convert(Lay::kOffV, v_full, v_empty, g + t - 1,
+      for (int t = 0; ok && t <= sp.tiles; ++t) {
+        if (t < sp.tiles) {
+          const uint32_t s = (g + t) % kStages;
+          ok = convert(Lay::kOffK + s * Lay::kTile, k_full0 + 8 * s,
+                       k_empty0 + 8 * s, (g + t) / kStages, kKeys);
+        }
+        if (ok && t >= 1) {
+          const uint32_t s = (g + t - 1) % kStages;
+          ok = convert(Lay::kOffV + s * Lay::kTile, v_full0 + 8 * s,
+                       v_empty0 + 8 * s, (g + t - 1) / kStages,
                        it.L - (t - 1) * kKeys);
+        }
       }
-      g += sp.n_tiles;
+      g += sp.tiles;
     }
     if (!ok) dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
     return;
@@ -540,27 +637,42 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // ---------------- softmax warps (thread = query row) ----------------
   regs_inc<kSoftmaxRegs>();
-  const int quarter = warp;  // tensor-memory lane quarter of this warp
+  const int x = warp >> 2;        // query tile of the pair
+  const int quarter = warp & 3;   // tensor-memory lane quarter of this warp
   const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t s_tmem = tbase + kColS + x * 64 + lane_off;
+  const uint32_t p_tmem = tbase + kColP + x * 32 + lane_off;
+  const uint32_t qt_tmem = tbase + kColQ + x * 32 + lane_off;
+  const uint32_t o_tmem = tbase + kColO + x * 128 + lane_off;
+  const uint32_t q_full = q_full0 + 8 * x, q_empty = q_empty0 + 8 * x;
+  const uint32_t s_full = s_full0 + 8 * x, s_free = s_free0 + 8 * x;
+  const uint32_t p_full = p_full0 + 8 * x, o_done = o_done0 + 8 * x;
   const int r = quarter * 32 + lane;
   const int t_loc = r / G;
   const int hg = r - t_loc * G;
-  auto wait_pv = [&](uint32_t t) {
-    return __all_sync(0xffffffffu, dev::mbar_wait(o_ready, t & 1));
-  };
   bool ok = true;
-  uint32_t g = 0;
-  int v = 0;
+  uint32_t g = 0;   // K/V tiles of this CTA's earlier items (scale slots)
+  uint32_t ts = 0;  // S tiles of this query tile so far
+  int v = 0;        // items so far
   for (int n = 0; ok; ++n) {
     Item it;
     ok = next_item(n, it);
     if (!ok || it.state == kEnd) break;
     if (it.state == kSkip) continue;
     const Span sp = span_of(it);
-    const int tok = sp.tok0 + t_loc;
-    const bool valid = t_loc < sp.n_q;
-    const int qpos = valid ? it.L - it.q_len + tok : sp.kv_end - 1;
-    const bool idle = quarter * 32 >= sp.n_q * G;
+    const int n_q = x ? sp.n_q[1] : sp.n_q[0];
+    const int n_tiles = x ? sp.n_tiles[1] : sp.n_tiles[0];
+    const int tok0 = x ? sp.tok0[1] : sp.tok0[0];
+    if (n_tiles == 0) {  // no rows for the second tile
+      g += sp.tiles;
+      continue;
+    }
+    const int tok = tok0 + t_loc;
+    const bool valid = t_loc < n_q;
+    // Padding rows see what the tile's last row sees; never stored.
+    const int qpos = it.L - it.q_len + (valid ? tok : tok0 + n_q - 1);
+    // A warp whose rows are all padding only keeps the barriers' protocol.
+    const bool idle = quarter * 32 >= n_q * G;
     const int64_t row_at =
         (static_cast<int64_t>(it.q0 + tok) * a.num_q_heads + it.kvh * G + hg) *
         D;
@@ -576,8 +688,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                              static_cast<const T*>(a.q) + row_at)[i]
                        : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (v >= 1 && !__all_sync(0xffffffffu,
-                                dev::mbar_wait(q_empty, (v - 1) & 1))) {
+      if (v >= 1 && !warp_wait(q_empty, (v - 1) & 1)) {
         ok = false;
         break;
       }
@@ -588,10 +699,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t top = 0u;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            top = __vmaxu2(top, x[e] & 0x7fff7fffu);
+            top = __vmaxu2(top, y[e] & 0x7fff7fffu);
         }
         const float2 top2 = dev::Mma<T>::unpack(top);
         const float amax = fmaxf(top2.x, top2.y);
@@ -601,20 +712,33 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float up =
             a.scale_log2 < 0.f ? -dev::exp2_int(k) : dev::exp2_int(k);
         c_row = fabsf(a.scale_log2) * dev::exp2_int(-k);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t y[4];
+        auto convert8 = [&](const uint4& in, uint32_t* z) {
+          const uint32_t y[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 f = dev::Mma<T>::unpack(x[e]);
-            y[e] = M::pack(f.x * up, f.y * up);
+            const float2 f = dev::Mma<T>::unpack(y[e]);
+            z[e] = M::pack(f.x * up, f.y * up);
           }
-          *reinterpret_cast<uint4*>(smem + Lay::kOffQ +
-                                    (i >> 3) * Lay::kHalfQ + r * 128 +
-                                    (((i & 7) ^ (r & 7)) << 4)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
+        };
+        constexpr int kInSmem = (kHalves - 1) * 8;  // 16-byte chunks
+#pragma unroll
+        for (int i = 0; i < kInSmem; ++i) {
+          uint32_t z[4];
+          convert8(w[i], z);
+          *reinterpret_cast<uint4*>(smem + Lay::kOffQ + x * Lay::kQTile +
+                                    r * 128 + ((i ^ (r & 7)) << 4)) =
+              make_uint4(z[0], z[1], z[2], z[3]);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t z[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            convert8(w[kInSmem + 4 * h + i], z + 4 * i);
+          dev::tmem_st16u(qt_tmem + 16 * h, z);
+        }
+        dev::tmem_st_wait();
+        dev::tc_fence_before();
         dev::fence_proxy_async_smem();
       }
       __syncwarp();
@@ -623,58 +747,54 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     float m_ref = -INFINITY, l = 0.f;
     int e_ref = 0;  // E
-    for (int j = 0; j < sp.n_tiles && ok; ++j) {
-      const uint32_t t = g + j;
-      ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full, t & 1));
+    for (int j = 0; j < n_tiles && ok; ++j, ++ts) {
+      ok = warp_wait(s_full, ts & 1);
       if (!ok) break;
       float sv[kKeys];
       if (!idle) {
         dev::tc_fence_after();
-        const uint32_t sa = s_tmem + lane_off;
         float (&lo)[32] = *reinterpret_cast<float(*)[32]>(sv);
         float (&hi)[32] = *reinterpret_cast<float(*)[32]>(sv + 32);
-        dev::tmem_ld32(sa, lo);
-        dev::tmem_ld32(sa + 32, hi);
+        dev::tmem_ld32(s_tmem, lo);
+        dev::tmem_ld32(s_tmem + 32, hi);
         dev::tmem_ld_wait();
         dev::tc_fence_before();
       }
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(s_free);
       if (idle) {
-        // Arrives for tile t only once P(t-1).V is done: an arrival a tile
-        // ahead would count toward tile t-1 on the single p_full barrier.
-        if (t >= 1 && !wait_pv(t - 1)) {
+        // Arrives for tile ts only once P(ts-1).V is done: an arrival a tile
+        // ahead would count toward tile ts-1 on the single p_full barrier.
+        if (ts >= 1 && !warp_wait(o_done, (ts - 1) & 1)) {
           ok = false;
           break;
         }
-        __syncwarp();
         if (lane == 0) dev::mbar_arrive(p_full);
         continue;
       }
-      const int k0 = j * kKeys;
-      const int lim = qpos - k0;
+      const int lim = qpos - j * kKeys;  // the last key this row sees
       if (lim < kKeys - 1) {
 #pragma unroll
         for (int k = 0; k < kKeys; ++k)
           if (k > lim) sv[k] = -INFINITY;
       }
-      // The tile's scales: a factor and an exponent per block.
+      // The tile's scales: a factor c_row ks_b (never 0: -inf * 0 is NaN) and
+      // log2(vs_b) for each block; the row's maximum, by blocks.
+      const float* sc = scale_s + ((g + j) % kScaleSlots) * 8;
       float cb[kNB], lv[kNB];
-      const float* sc = scale_s + (t % kScaleSlots) * 8;
       float mx = -INFINITY, top = -100.f;
 #pragma unroll
       for (int b = 0; b < kNB; ++b) {
-        cb[b] = fmaxf(c_row * sc[b], 1.1754944e-38f);  // -inf * 0 is NaN
+        cb[b] = fmaxf(c_row * sc[b], 1.1754944e-38f);
         lv[b] = sc[kNB + b];
         top = fmaxf(top, lv[b]);
         float m4[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u) {
           m4[u] = dev::fmax3(sv[b * BS + u], sv[b * BS + 4 + u],
                              sv[b * BS + 8 + u]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
           m4[u] = fmaxf(m4[u], sv[b * BS + 12 + u]);
+        }
         if constexpr (BS == 32) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -704,58 +824,53 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (__any_sync(0xffffffffu, factor != 1.f)) {
-        ok = wait_pv(t - 1);
-        if (!ok) break;
-        dev::tc_fence_after();
         // Rare (the maxima settle): a rolled loop over 16 columns, which
         // leaves the scores in their registers.
+        ok = warp_wait(o_done, (ts - 1) & 1);
+        if (!ok) break;
+        dev::tc_fence_after();
 #pragma unroll 1
         for (int col = 0; col < D; col += 16) {
           uint32_t ov[16];
-          dev::tmem_ld16u(o_tmem + lane_off + col, ov);
+          dev::tmem_ld16u(o_tmem + col, ov);
           dev::tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
-          dev::tmem_st16u(o_tmem + lane_off + col, ov);
+          dev::tmem_st16u(o_tmem + col, ov);
         }
-        dev::tmem_st_wait();
       }
       // w = 2^(s c_b + log2(vs_b) - E + shift - m), two keys per
       // instruction; the sum of p from the block sums of w.
-      {
-        uint32_t hw[kKeys / 2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h) {
+        uint32_t hw[16];
 #pragma unroll
-          for (int b = h * kNB / 2; b < (h + 1) * kNB / 2; ++b) {
-            const float lvn =
-                fmaxf(lv[b] - static_cast<float>(e_ref), -96.f) + kShift;
-            const float off = lvn - m_ref;
-            const float2 c2 = make_float2(cb[b], cb[b]);
-            const float2 o2 = make_float2(off, off);
-            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int b = h * kNB / 2; b < (h + 1) * kNB / 2; ++b) {
+          const float lvn =
+              fmaxf(lv[b] - static_cast<float>(e_ref), -96.f) + kShift;
+          const float off = lvn - m_ref;
+          const float2 c2 = make_float2(cb[b], cb[b]);
+          const float2 o2 = make_float2(off, off);
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int e = b * BS / 2; e < (b + 1) * BS / 2; ++e) {
-              const float2 x =
-                  dev::ffma2(make_float2(sv[2 * e], sv[2 * e + 1]), c2, o2);
-              const float w0 = dev::fast_exp2(x.x), w1 = dev::fast_exp2(x.y);
-              l2[e & 1] = dev::fadd2(l2[e & 1], make_float2(w0, w1));
-              hw[e] = M::pack(w0, w1);
-            }
-            const float2 lb = dev::fadd2(l2[0], l2[1]);
-            l = fmaf(lb.x + lb.y, dev::fast_exp2(-lvn), l);
+          for (int e = b * BS / 2; e < (b + 1) * BS / 2; ++e) {
+            const float2 y =
+                dev::ffma2(make_float2(sv[2 * e], sv[2 * e + 1]), c2, o2);
+            const float w0 = dev::fast_exp2(y.x), w1 = dev::fast_exp2(y.y);
+            l2[e & 1] = dev::fadd2(l2[e & 1], make_float2(w0, w1));
+            hw[e - 16 * h] = M::pack(w0, w1);
           }
-          if (h == 0) {
-            // P(t-1).V must have read the P buffer before it is overwritten.
-            if (t >= 1 && !wait_pv(t - 1)) ok = false;
-            if (!ok) break;
-            dev::tc_fence_after();
-          }
-          dev::tmem_st16u(
-              p_tmem + lane_off + 16 * h,
-              *reinterpret_cast<const uint32_t(*)[16]>(hw + 16 * h));
+          const float2 lb = dev::fadd2(l2[0], l2[1]);
+          l = fmaf(lb.x + lb.y, dev::fast_exp2(-lvn), l);
         }
+        if (h == 0) {
+          // P(ts-1).V must have read the P buffer before it is overwritten.
+          if (ts >= 1 && !warp_wait(o_done, (ts - 1) & 1)) ok = false;
+          if (!ok) break;
+          dev::tc_fence_after();
+        }
+        dev::tmem_st16u(p_tmem + 16 * h, hw);
       }
       if (!ok) break;
       dev::tmem_st_wait();
@@ -764,7 +879,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) dev::mbar_arrive(p_full);
     }
     // The item's output: O 2^(E - shift) / l -> out[token, query head].
-    if (ok && !idle) ok = wait_pv(g + sp.n_tiles - 1);
+    // (The phase before it was waited for with the last tile's P.)
+    if (ok) ok = warp_wait(o_done, (ts - 1) & 1);
     if (ok && !idle) {
       dev::tc_fence_after();
       // l is above 0 (each row sees a key) or NaN, which is passed on
@@ -774,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int col = 0; col < D; col += 32) {
         float ov[32];
-        dev::tmem_ld32(o_tmem + lane_off + col, ov);
+        dev::tmem_ld32(o_tmem + col, ov);
         dev::tmem_ld_wait();
         if (valid && a.out_f32) {
 #pragma unroll
@@ -794,8 +910,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
+      dev::tc_fence_before();
     }
-    g += sp.n_tiles;
+    g += sp.tiles;
   }
   if (!ok) dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
   dev::tc_fence_before();
@@ -823,7 +940,7 @@ pa_status launch(const PrefillQ8Args& a, cudaStream_t st) {
     return fail(PA_ERR_CUDA, "pa_prefill_q8: cudaFuncSetAttribute(%zu): %s",
                 smem, cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
-  const int64_t slots = 2LL * std::max(device_sm_count(), 1);
+  const int64_t slots = std::max(device_sm_count(), 1);  // one CTA per SM
   cfg.gridDim =
       dim3(static_cast<unsigned>(std::min<int64_t>(a.num_items, slots)));
   cfg.blockDim = dim3(kThreads);
@@ -894,7 +1011,11 @@ extern "C" pa_status pa_prefill_q8(
   a.v_scales = v_scales;
   a.tiles = pagedkv::tile_map(d, workspace);
   a.counter = pagedkv::work_counter(d, workspace);
-  a.num_items = static_cast<int>(pagedkv::tile_cap(d) * d->num_kv_heads);
+  // Items of kPair query tiles: the tile map holds at most as many entries
+  // as with tiles of one, for which the workspace is sized.
+  const int item_tok = pagedkv::kPair * pagedkv::tile_tokens(d);
+  const int64_t cap = pagedkv::tile_cap(d, item_tok);
+  a.num_items = static_cast<int>(cap * d->num_kv_heads);
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.query_start = query_start;
@@ -910,7 +1031,7 @@ extern "C" pa_status pa_prefill_q8(
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const pa_status planned =
       pagedkv::launch_plan("pa_prefill_q8", d, context_lens, query_start,
-                           max_ctx, workspace, dev_err, s);
+                           max_ctx, item_tok, workspace, dev_err, s);
   if (planned != PA_OK) return planned;
   return d->dtype == PA_BF16
              ? pagedkv::dispatch_shape<__nv_bfloat16>(d, a, s)
