@@ -70,6 +70,10 @@ constexpr int kLaunchRegs = 128;
 constexpr int kSoftmaxRegs = 192, kConvRegs = 48, kIssueRegs = 80;
 static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs == 4 * kLaunchRegs,
               "more registers than the block was launched with");
+// What the page warp stages for a tile: for each of its blocks ks, the
+// exponent log2(vs) - E + kShift and 2^-that; then the factor of O for a
+// grown E, and E.
+constexpr int kSlotFloats = 16;
 // Tensor memory columns, for each query tile: S 64, P 32, the last 64 dims of
 // q 32, O head_dim (up to 128).
 constexpr int kTmemCols = 512;
@@ -123,7 +127,7 @@ struct LayoutQ8 {
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kOffRaw = kOffV + kStages * kTile;
   static constexpr int kOffScales = kOffRaw + kRaw * kRawTile;
-  static constexpr int kOffBars = kOffScales + kScaleSlots * 32;
+  static constexpr int kOffBars = kOffScales + kScaleSlots * kSlotFloats * 4;
   static constexpr size_t kSmemBytes =
       1024 + kOffBars + kNumBars * 8 + 16 + 2 * kItemWords * 4;
 };
@@ -140,8 +144,8 @@ __device__ __forceinline__ void regs_dec() {
 
 constexpr uint32_t kSuspendNs = 20000;
 
-// dev::mbar_wait with a suspend-time hint: a waiting thread sleeps in the
-// barrier instead of polling it, which leaves the issue slots to the others.
+// A try_wait with a suspend-time hint: a waiting thread sleeps in the barrier
+// instead of polling it, which leaves the issue slots to the others.
 __device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -153,13 +157,26 @@ __device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
-  if (try_wait_hint(bar, parity)) return true;
+// By a whole warp, converged: every branch is uniform (a wait each lane loops
+// on by itself costs about 250 cycles even when there is nothing to wait
+// for), and so is the result, which collectives follow.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, try_wait_hint(bar, parity))) return true;
   const uint64_t t0 = dev::globaltimer();
-  while (!try_wait_hint(bar, parity)) {
-    if (dev::globaltimer() - t0 > dev::kWaitLimitNs) return false;
+  for (;;) {
+    if (__all_sync(0xffffffffu, try_wait_hint(bar, parity))) return true;
+    if (__any_sync(0xffffffffu,
+                   dev::globaltimer() - t0 > dev::kWaitLimitNs))
+      return false;
   }
-  return true;
+}
+// One arrival for a converged warp, without a branch.  (What it publishes is
+// ordered by the caller: a warp-wide tcgen05 wait, or __syncwarp.)
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // `bytes` contiguous bytes global -> shared, counted on `bar`.
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto read_item = [&](int n, Item& it) -> bool {
     const int slot = n & 1;
-    if (!wait_bar(item_full0 + 8 * slot, (n >> 1) & 1)) return false;
+    if (!warp_wait(item_full0 + 8 * slot, (n >> 1) & 1)) return false;
     const volatile int* d = item_s + kItemWords * slot;
     it.state = d[0];
     it.b = d[1];
@@ -285,14 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.q_len = d[6];
     return true;
   };
-  // Waits of a whole warp, with a warp-uniform result (collectives follow).
-  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity));
-  };
   auto next_item = [&](int n, Item& it) -> bool {
-    if (!__all_sync(0xffffffffu, read_item(n, it))) return false;
+    if (!read_item(n, it)) return false;
     __syncwarp();
-    if (lane == 0) dev::mbar_arrive(item_empty0 + 8 * (n & 1));
+    warp_arrive(item_empty0 + 8 * (n & 1));
     return true;
   };
 
@@ -388,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Ids are read two tiles and scales one tile ahead of their use.
       int32_t cur = 0, nxt = 0, nn = 0, prv = 0;
+      int e_ref = 0;  // E
       float2 sc = make_float2(1.f, 0.f), nsc = sc;
       if (mine) {
         nxt = fetch(0);
@@ -409,10 +423,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           // at most two tiles ahead of the one being converted, which is at
           // most kStages ahead of the one whose S is next, at most two ahead
           // of the one in the softmax: the slot's old readers are past it.
+          const float lv =
+              mine ? fminf(fmaxf(log2f(sc.y), -100.f), 100.f) : -100.f;
+          float top = lv;
+#pragma unroll
+          for (int m = 1; m < kNB; m <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+          const int e_top =
+              static_cast<int>(floorf(__shfl_sync(0xffffffffu, top, 0)));
+          int grow = 0;
+          if (t == 0) {
+            e_ref = e_top;
+          } else if (e_top > e_ref + kVsSlack) {
+            grow = max(e_ref - e_top, -126);
+            e_ref = e_top;
+          }
+          float* to = scale_s + ((g + t) % kScaleSlots) * kSlotFloats;
           if (mine) {
-            float* to = scale_s + ((g + t) % kScaleSlots) * 8;
+            const float lvn =
+                fmaxf(lv - static_cast<float>(e_ref), -96.f) + kShift;
             to[p] = sc.x;
-            to[kNB + p] = fminf(fmaxf(log2f(sc.y), -100.f), 100.f);
+            to[kNB + p] = lvn;
+            to[2 * kNB + p] = exp2f(-lvn);
+          }
+          if (lane == 0) {
+            to[kSlotFloats - 2] = dev::exp2_int(grow);
+            to[kSlotFloats - 1] = static_cast<float>(e_ref);
           }
           copy(a.k_cache, kvh, cur);
         }
@@ -435,8 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kMmaWarp + kPair) return;
   if (warp >= kMmaWarp) {
     // ---------------- MMA issuers, one per query tile ----------------
-    if (lane == 0) {
-      const int x = warp - kMmaWarp;
+    // The whole warp runs this, with uniform values; one thread issues.
+    {
+      const int x = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
+      const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_slot, 0);
       bool ok = true;
       constexpr uint32_t idesc_qk =
           dev::umma_idesc_f16(false, kRows, kKeys, false, false);
@@ -462,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // bounds the other form.
       auto issue_s = [&](uint32_t t, bool last) -> bool {
         const uint32_t s = t % kStages;
-        if (!wait_bar(k_full0 + 8 * s, (t / kStages) & 1) ||
-            (ts >= 1 && !wait_bar(s_free, (ts - 1) & 1)))
+        if (!warp_wait(k_full0 + 8 * s, (t / kStages) & 1) ||
+            (ts >= 1 && !warp_wait(s_free, (ts - 1) & 1)))
           return false;
         dev::tc_fence_after();
         const uint64_t k = kd + s * (Lay::kTile >> 4);
@@ -472,64 +510,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int h = kk >> 2, k4 = kk & 3;
           const uint64_t kb = k + ((h * kTileHalf + k4 * 32) >> 4);
           if (h + 1 < kHalves)
-            dev::umma_f16(s_tmem, qd + ((h * kRows * 128 + k4 * 32) >> 4), kb,
+            dev::umma_f16_warp(s_tmem, qd + ((h * kRows * 128 + k4 * 32) >> 4), kb,
                           idesc_qk, kk > 0 ? 1u : 0u);
           else
-            dev::umma_f16_ts(s_tmem, qt_tmem + k4 * 8, kb, idesc_qk,
+            dev::umma_f16_ts_warp(s_tmem, qt_tmem + k4 * 8, kb, idesc_qk,
                              kk > 0 ? 1u : 0u);
         }
-        dev::umma_commit(s_full);
-        dev::umma_commit(k_empty0 + 8 * s);
-        if (last) dev::umma_commit(q_empty0 + 8 * x);
+        dev::umma_commit_warp(s_full);
+        dev::umma_commit_warp(k_empty0 + 8 * s);
+        if (last) dev::umma_commit_warp(q_empty0 + 8 * x);
         ++ts;
         return true;
       };
       // O (+)= P(t) V(t); p: P's phase.
       auto issue_pv = [&](uint32_t t, uint32_t p, bool first) -> bool {
         const uint32_t s = t % kStages;
-        if (!wait_bar(v_full0 + 8 * s, (t / kStages) & 1) ||
-            !wait_bar(p_full, p & 1))
+        if (!warp_wait(v_full0 + 8 * s, (t / kStages) & 1) ||
+            !warp_wait(p_full, p & 1))
           return false;
         dev::tc_fence_after();
         const uint64_t vb = vd + s * (Lay::kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          dev::umma_f16_ts(o_tmem, p_tmem + kk * 8, vb + kk * (2048 >> 4),
+          dev::umma_f16_ts_warp(o_tmem, p_tmem + kk * 8, vb + kk * (2048 >> 4),
                            idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        dev::umma_commit(o_done);
-        dev::umma_commit(v_empty0 + 8 * s);
+        dev::umma_commit_warp(o_done);
+        dev::umma_commit_warp(v_empty0 + 8 * s);
         return true;
       };
       // A tile this query tile does not see (the other one does): only its
       // share of the release, once the tile's phase has begun.
       auto skip = [&](uint32_t t, uint32_t full0, uint32_t empty0) -> bool {
         const uint32_t s = t % kStages;
-        if (!wait_bar(full0 + 8 * s, (t / kStages) & 1)) return false;
-        dev::mbar_arrive(empty0 + 8 * s);
+        if (!warp_wait(full0 + 8 * s, (t / kStages) & 1)) return false;
+        warp_arrive(empty0 + 8 * s);
         return true;
       };
       for (int n = 0; ok; ++n) {
         Item it;
-        if (!read_item(n, it)) {
-          ok = false;
-          break;
-        }
-        dev::mbar_arrive(item_empty0 + 8 * (n & 1));
-        if (it.state == kEnd) break;
+        ok = next_item(n, it);
+        if (!ok || it.state == kEnd) break;
         if (it.state == kSkip) continue;
         const Span sp = span_of(it);
-        const int nt = x ? sp.n_tiles[1] : sp.n_tiles[0];
+        const int nt =
+            __shfl_sync(0xffffffffu, x ? sp.n_tiles[1] : sp.n_tiles[0], 0);
+        const int tiles = __shfl_sync(0xffffffffu, sp.tiles, 0);
         if (nt > 0) {
-          ok = wait_bar(q_full0 + 8 * x, v & 1) && issue_s(g, nt == 1);
+          ok = warp_wait(q_full0 + 8 * x, v & 1) && issue_s(g, nt == 1);
           ++v;
         } else {
           ok = skip(g, k_full0, k_empty0);
         }
         // S(j+1) goes ahead of P(j).V, which waits for the softmax.
-        for (int j = 0; ok && j < sp.tiles; ++j) {
+        for (int j = 0; ok && j < tiles; ++j) {
           if (j + 1 < nt)
             ok = issue_s(g + j + 1, j + 2 == nt);
-          else if (j + 1 < sp.tiles)
+          else if (j + 1 < tiles)
             ok = skip(g + j + 1, k_full0, k_empty0);
           if (!ok) break;
           if (j < nt)
@@ -537,12 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             ok = skip(g + j, v_full0, v_empty0);
         }
-        g += sp.tiles;
+        g += tiles;
       }
-      if (!ok) dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
       // Tensor memory is released once the softmax warps are done with it;
       // they have then seen their last P.V complete.
-      if (!wait_bar(done, 0)) dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
+      if (!warp_wait(done, 0)) ok = false;
+      if (!ok && lane == 0)
+        dev::set_error(a.dev_err, PA_ERR_DEVICE_TIMEOUT);
     }
     __syncwarp();
     dev::tc_fence_after();
@@ -603,10 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       dev::fence_proxy_async_smem();  // visible to the tensor cores
       __syncwarp();
-      if (lane == 0) {
-        dev::mbar_arrive(full);
-        dev::mbar_arrive(raw_empty0 + 8 * slot);
-      }
+      warp_arrive(full);
+      warp_arrive(raw_empty0 + 8 * slot);
       ++u;
       return true;
     };
@@ -742,11 +777,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         dev::fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(q_full);
+      warp_arrive(q_full);
       ++v;
     }
     float m_ref = -INFINITY, l = 0.f;
-    int e_ref = 0;  // E
     for (int j = 0; j < n_tiles && ok; ++j, ++ts) {
       ok = warp_wait(s_full, ts & 1);
       if (!ok) break;
@@ -760,8 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         dev::tmem_ld_wait();
         dev::tc_fence_before();
       }
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(s_free);
+      warp_arrive(s_free);
       if (idle) {
         // Arrives for tile ts only once P(ts-1).V is done: an arrival a tile
         // ahead would count toward tile ts-1 on the single p_full barrier.
@@ -769,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        if (lane == 0) dev::mbar_arrive(p_full);
+        warp_arrive(p_full);
         continue;
       }
       const int lim = qpos - j * kKeys;  // the last key this row sees
@@ -778,16 +811,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kKeys; ++k)
           if (k > lim) sv[k] = -INFINITY;
       }
-      // The tile's scales: a factor c_row ks_b (never 0: -inf * 0 is NaN) and
-      // log2(vs_b) for each block; the row's maximum, by blocks.
-      const float* sc = scale_s + ((g + j) % kScaleSlots) * 8;
-      float cb[kNB], lv[kNB];
-      float mx = -INFINITY, top = -100.f;
+      // The row's maximum, by blocks: a factor c_row ks_b for each (never 0:
+      // -inf * 0 is NaN).
+      const float* sc = scale_s + ((g + j) % kScaleSlots) * kSlotFloats;
+      float cb[kNB];
+      float mx = -INFINITY;
 #pragma unroll
       for (int b = 0; b < kNB; ++b) {
         cb[b] = fmaxf(c_row * sc[b], 1.1754944e-38f);
-        lv[b] = sc[kNB + b];
-        top = fmaxf(top, lv[b]);
         float m4[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -807,21 +838,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) *
                            cb[b]);
       }
-      float factor = 1.f;
-      const int e_top = static_cast<int>(floorf(top));
+      float factor = sc[kSlotFloats - 2];  // 1, or what E grew by
       if (j == 0) {
         m_ref = mx;  // O is still empty: the first P.V overwrites it
-        e_ref = e_top;
-      } else {
-        if (mx > m_ref + kRescaleLog2) {
-          factor = dev::fast_exp2(m_ref - mx);
-          m_ref = mx;
-          l *= factor;
-        }
-        if (e_top > e_ref + kVsSlack) {
-          factor *= dev::exp2_int(max(e_ref - e_top, -126));
-          e_ref = e_top;
-        }
+      } else if (mx > m_ref + kRescaleLog2) {
+        const float f = dev::fast_exp2(m_ref - mx);
+        m_ref = mx;
+        l *= f;
+        factor *= f;
       }
       if (__any_sync(0xffffffffu, factor != 1.f)) {
         // Rare (the maxima settle): a rolled loop over 16 columns, which
@@ -847,9 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t hw[16];
 #pragma unroll
         for (int b = h * kNB / 2; b < (h + 1) * kNB / 2; ++b) {
-          const float lvn =
-              fmaxf(lv[b] - static_cast<float>(e_ref), -96.f) + kShift;
-          const float off = lvn - m_ref;
+          const float off = sc[kNB + b] - m_ref;
           const float2 c2 = make_float2(cb[b], cb[b]);
           const float2 o2 = make_float2(off, off);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -862,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             hw[e - 16 * h] = M::pack(w0, w1);
           }
           const float2 lb = dev::fadd2(l2[0], l2[1]);
-          l = fmaf(lb.x + lb.y, dev::fast_exp2(-lvn), l);
+          l = fmaf(lb.x + lb.y, sc[2 * kNB + b], l);
         }
         if (h == 0) {
           // P(ts-1).V must have read the P buffer before it is overwritten.
@@ -875,8 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       dev::tmem_st_wait();
       dev::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(p_full);
+      warp_arrive(p_full);
     }
     // The item's output: O 2^(E - shift) / l -> out[token, query head].
     // (The phase before it was waited for with the last tile's P.)
@@ -884,7 +905,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && !idle) {
       dev::tc_fence_after();
       // l is above 0 (each row sees a key) or NaN, which is passed on
-      const float inv = dev::exp2_int(e_ref - static_cast<int>(kShift)) / l;
+      const float e_last = scale_s[((g + n_tiles - 1) % kScaleSlots) *
+                                       kSlotFloats + kSlotFloats - 1];
+      const float inv =
+          dev::exp2_int(static_cast<int>(e_last - kShift)) / l;
       T* dst = static_cast<T*>(a.out) + row_at;
       float* dst32 = static_cast<float*>(a.out) + row_at;  // out_f32 only
 #pragma unroll
