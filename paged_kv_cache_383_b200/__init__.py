@@ -397,35 +397,62 @@ _ROPE_SCALINGS = {None: _lib.PA_ROPE_PLAIN, "linear": _lib.PA_ROPE_LINEAR,
                   "yarn": _lib.PA_ROPE_YARN}
 
 
-def _on_current(*named):
-    """Pointers of contiguous tensors that live on the current device
-    (``(tensor, name, dtype or None)`` each; None tensors give NULL).  The
-    library launches there: a tensor of another device is refused."""
+# What the calls below ask of torch on every call, looked up once: a decode
+# step's device work is a few microseconds, as much as a few dozen Python
+# attribute lookups.
+_tc: dict = {}
+
+
+def _torch_refs():
     import torch
-    dev = torch.cuda.current_device()
-    out = []
-    for t, name, dtype in named:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on the current "
-                             f"device (cuda:{dev}), is on {t.device}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        out.append(t.data_ptr())
-    return out
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def raw(dev):
+            return torch.cuda.current_stream(dev).cuda_stream
+    _tc.update(device=torch.cuda.current_device, raw_stream=raw,
+               i32=torch.int32, f32=torch.float32, f64=torch.float64,
+               e4m3=torch.float8_e4m3fn,
+               codes={torch.float16: PA_F16, torch.bfloat16: PA_BF16},
+               empty=torch.empty, u8=torch.uint8)
+    return _tc
+
+
+def _ptr(t, name: str, dev: int, dtype=None):
+    """Pointer of a contiguous tensor on device ``dev``, the current one: the
+    library launches there, so a tensor of another device is refused.  None
+    gives NULL."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current "
+                         f"device (cuda:{dev}), is on {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _stream_on(stream, dev: int) -> int:
+    if stream is None:
+        return _tc["raw_stream"](dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _code(dt) -> int:
+    code = _tc["codes"].get(dt)
+    if code is None:
+        raise TypeError(f"expected float16 or bfloat16, got {dt}")
+    return code
 
 
 def _workspace(need: int, device, stream):
     """A workspace of the call's own.  torch hands its memory out again on
     the stream it was allocated on, so one used on another stream is marked
     as in use there."""
-    import torch
-    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    ws = _tc["empty"](max(need, 16), dtype=_tc["u8"], device=device)
     if stream is not None:
+        import torch
         s = torch.cuda.ExternalStream(stream, device=device) \
             if isinstance(stream, int) else stream
         if s != torch.cuda.current_stream():
@@ -467,32 +494,36 @@ def pa_rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling=None,
     return torch.tensor(list(out), dtype=torch.float64), float(sc.value)
 
 
-def _rows(t, name: str, heads: int, head_dim: int, total: int, dt):
-    """Row stride of a [total, heads, head_dim] tensor whose heads are dense
-    within a row (a slice of a projection's output, say)."""
-    if t.shape != (total, heads, head_dim):
-        raise ValueError(f"{name} must be [{total}, {heads}, {head_dim}], is "
-                         f"{list(t.shape)}")
+def _rows(t, name: str, shape, dt, dev: int):
+    """(pointer, row stride) of a [rows, heads, head_dim] tensor whose heads
+    are dense within a row (a slice of a projection's output, say)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
     if t.dtype != dt:
         raise TypeError(f"{name} dtype {t.dtype} != {dt}")
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and head_dim > 1) or (s1 != head_dim and heads > 1):
+    rows, heads, head_dim = shape
+    if s2 != 1 or (s1 != head_dim and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be dense "
                          f"(strides {t.stride()})")
-    return s0 if total > 1 else heads * head_dim
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current "
+                         f"device (cuda:{dev}), is on {t.device}")
+    return t.data_ptr(), s0 if rows > 1 else heads * head_dim
 
 
 def _append(fn, name, q_out, k_cache, v_cache, scales, q, k, v, block_tables,
             context_lens, query_start, max_q_len, q_norm, k_norm, norm_eps,
             rope_freqs, rope_layout, rope_scale, dev_err, stream):
-    import torch
-    num_blocks, hkv, block_size, head_dim = k_cache.shape
-    if v_cache.shape != k_cache.shape:
+    tc = _tc or _torch_refs()
+    shape = k_cache.shape
+    num_blocks, hkv, block_size, head_dim = shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache differ in shape")
     total, dt = k.shape[0], k.dtype
     num_seqs = context_lens.shape[0]
-    if context_lens.dim() != 1 or block_tables.dim() != 2 or \
-            block_tables.shape[0] != num_seqs:
+    bt = block_tables.shape
+    if context_lens.dim() != 1 or len(bt) != 2 or bt[0] != num_seqs:
         raise ValueError("context_lens must be [num_seqs] and block_tables "
                          "[num_seqs, max_blocks_per_seq]")
     if query_start is None:
@@ -505,18 +536,26 @@ def _append(fn, name, q_out, k_cache, v_cache, scales, q, k, v, block_tables,
             raise ValueError("query_start must be [num_seqs + 1]")
         if max_q_len is None:
             max_q_len = total
-    if rope_layout not in _ROPE_LAYOUTS:
+    layout = _ROPE_LAYOUTS.get(rope_layout)
+    if layout is None:
         raise ValueError(f"rope_layout {rope_layout!r} is none of "
                          f"{list(_ROPE_LAYOUTS)}")
-    ks = _rows(k, "k", hkv, head_dim, total, dt)
-    vs = _rows(v, "v", hkv, head_dim, total, dt)
-    hq = qs = os = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
+    dev = k_cache.get_device()
+    kv_shape = (total, hkv, head_dim)
+    k_ptr, ks = _rows(k, "k", kv_shape, dt, dev)
+    v_ptr, vs = _rows(v, "v", kv_shape, dt, dev)
+    hq = qs = os = 0
+    q_ptr = out_ptr = None
     if q is not None:
         hq = q.shape[1]
-        qs = _rows(q, "q", hq, head_dim, total, dt)
-        os = _rows(q_out, "q_out", hq, head_dim, total, dt)
+        q_shape = (total, hq, head_dim)
+        q_ptr, qs = _rows(q, "q", q_shape, dt, dev)
+        out_ptr, os = _rows(q_out, "q_out", q_shape, dt, dev)
+    if dev != tc["device"]():
+        raise ValueError(f"the caches are on {k_cache.device}, which is not "
+                         "the current CUDA device")
     for w, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if w is not None and w.shape != (head_dim,):
             raise ValueError(f"{n} must be [{head_dim}]")
@@ -525,29 +564,24 @@ def _append(fn, name, q_out, k_cache, v_cache, scales, q, k, v, block_tables,
         if rope_freqs.dim() != 1:
             raise ValueError("rope_freqs must be [rot_dim / 2]")
         rot_dim = 2 * rope_freqs.shape[0]
+    i32 = tc["i32"]
+    cache_dt = tc["e4m3"] if scales else dt
     desc = _lib.pa_append_desc(
-        num_seqs, hq, hkv, head_dim, block_size, block_tables.shape[1],
-        num_blocks, _dtype_code(k), total, max_q_len, rot_dim,
-        _ROPE_LAYOUTS[rope_layout], rope_scale, norm_eps, qs, ks, vs, os)
-    cache_dt = torch.float8_e4m3fn if scales else dt
-    ptrs = _on_current(
-        (k_cache, "k_cache", cache_dt), (v_cache, "v_cache", cache_dt),
-        *scales, (q_norm, "q_norm", dt), (k_norm, "k_norm", dt),
-        (rope_freqs, "rope_freqs", torch.float64),
-        (block_tables, "block_tables", torch.int32),
-        (context_lens, "context_lens", torch.int32),
-        (query_start, "query_start", torch.int32),
-        (dev_err, "dev_err", torch.int32))
-    dev = k_cache.get_device()
-    rows = []
-    for t, n in ((q_out, "q_out"), (q, "q"), (k, "k"), (v, "v")):
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{n} is on {t.device}, not cuda:{dev}")
-        rows.append(None if t is None else t.data_ptr())
-    n = 2 + len(scales)
-    st = fn(rows[0], *ptrs[:n], *rows[1:], *ptrs[n:-1], ctypes.byref(desc),
-            ptrs[-1], _stream(stream))
-    _lib.check(st, name)
+        num_seqs, hq, hkv, head_dim, block_size, bt[1], num_blocks, _code(dt),
+        total, max_q_len, rot_dim, layout, rope_scale, norm_eps, qs, ks, vs,
+        os)
+    st = fn(out_ptr, _ptr(k_cache, "k_cache", dev, cache_dt),
+            _ptr(v_cache, "v_cache", dev, cache_dt),
+            *[_ptr(t, n, dev, tc["f32"]) for t, n in scales],
+            q_ptr, k_ptr, v_ptr, _ptr(q_norm, "q_norm", dev, dt),
+            _ptr(k_norm, "k_norm", dev, dt),
+            _ptr(rope_freqs, "rope_freqs", dev, tc["f64"]),
+            _ptr(block_tables, "block_tables", dev, i32),
+            _ptr(context_lens, "context_lens", dev, i32),
+            _ptr(query_start, "query_start", dev, i32), ctypes.byref(desc),
+            _ptr(dev_err, "dev_err", dev, i32), _stream_on(stream, dev))
+    if st:
+        _lib.check(st, name)
     return q_out
 
 
@@ -578,11 +612,9 @@ def pa_append_q8(q_out, k_cache, v_cache, k_scales, v_scales, q, k, v,
     """``pa_append`` into the 8-bit cache: e4m3 codes and one power-of-two
     scale per (block, KV head), older codes of a block following a scale
     that grows.  Returns ``q_out``."""
-    import torch
     _check_q8(k_cache, v_cache, k_scales, v_scales)
     return _append(_lib.load().pa_append_q8, "pa_append_q8", q_out, k_cache,
-                   v_cache, ((k_scales, "k_scales", torch.float32),
-                             (v_scales, "v_scales", torch.float32)),
+                   v_cache, ((k_scales, "k_scales"), (v_scales, "v_scales")),
                    q, k, v, block_tables, context_lens, query_start,
                    max_q_len, q_norm, k_norm, norm_eps, rope_freqs,
                    rope_layout, rope_scale, dev_err, stream)
@@ -590,19 +622,24 @@ def pa_append_q8(q_out, k_cache, v_cache, k_scales, v_scales, q, k, v,
 
 def _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
                     block_tables, context_lens, workspace, dev_err):
-    import torch
+    """(device, the eight tensors' pointers, workspace, dev_err)."""
+    tc = _tc
     _check_q8(k_cache, v_cache, k_scales, v_scales)
     if out.shape != q.shape:
         raise ValueError("q and out disagree on shape")
     if context_lens.shape != block_tables.shape[:1]:
         raise ValueError("context_lens must be [num_seqs]")
-    e4m3, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
-    return _on_current(
-        (out, "out", None), (q, "q", None), (k_cache, "k_cache", e4m3),
-        (v_cache, "v_cache", e4m3), (k_scales, "k_scales", f32),
-        (v_scales, "v_scales", f32), (block_tables, "block_tables", i32),
-        (context_lens, "context_lens", i32), (workspace, "workspace", None),
-        (dev_err, "dev_err", i32))
+    e4m3, f32, i32 = tc["e4m3"], tc["f32"], tc["i32"]
+    dev = tc["device"]()
+    return (dev, _ptr(out, "out", dev), _ptr(q, "q", dev),
+            _ptr(k_cache, "k_cache", dev, e4m3),
+            _ptr(v_cache, "v_cache", dev, e4m3),
+            _ptr(k_scales, "k_scales", dev, f32),
+            _ptr(v_scales, "v_scales", dev, f32),
+            _ptr(block_tables, "block_tables", dev, i32),
+            _ptr(context_lens, "context_lens", dev, i32),
+            _ptr(workspace, "workspace", dev), _ptr(dev_err, "dev_err", dev,
+                                                    i32))
 
 
 def pa_decode_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
@@ -614,6 +651,7 @@ def pa_decode_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
     tensor of ``pa_decode_workspace_bytes`` bytes) is allocated per call when
     not given.  Returns ``out``."""
     lib = _lib.load()
+    _tc or _torch_refs()
     if desc is None:
         desc = make_desc(q, k_cache, block_tables,
                          partition_size=partition_size,
@@ -623,12 +661,12 @@ def pa_decode_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
         workspace = _workspace(
             int(lib.pa_decode_workspace_bytes(ctypes.byref(desc))), q.device,
             stream)
-    p = _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
-                        block_tables, context_lens, workspace, dev_err)
-    st = lib.pa_decode_q8(
-        *p[:8], scale, ctypes.byref(desc), p[8],
-        workspace.numel() * workspace.element_size(), p[9], _stream(stream))
-    _lib.check(st, "pa_decode_q8")
+    dev, *p = _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
+                              block_tables, context_lens, workspace, dev_err)
+    st = lib.pa_decode_q8(*p[:8], scale, ctypes.byref(desc), p[8],
+                          workspace.nbytes, p[9], _stream_on(stream, dev))
+    if st:
+        _lib.check(st, "pa_decode_q8")
     return out
 
 
@@ -639,8 +677,8 @@ def pa_prefill_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
     """``pa_prefill`` over the 8-bit cache.  ``workspace`` (a uint8 CUDA
     tensor of ``pa_prefill_workspace_bytes`` bytes) is allocated per call
     when not given.  Returns ``out``."""
-    import torch
     lib = _lib.load()
+    _tc or _torch_refs()
     if query_start.shape != (block_tables.shape[0] + 1,):
         raise ValueError("query_start must be [num_seqs + 1]")
     desc = _prefill_desc(q, k_cache, block_tables, max_q_len,
@@ -650,13 +688,14 @@ def pa_prefill_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
         workspace = _workspace(
             lib.pa_prefill_workspace_bytes(ctypes.byref(desc)), q.device,
             stream)
-    p = _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
-                        block_tables, context_lens, workspace, dev_err)
-    qs, = _on_current((query_start, "query_start", torch.int32))
+    dev, *p = _attend_q8_ptrs(out, q, k_cache, v_cache, k_scales, v_scales,
+                              block_tables, context_lens, workspace, dev_err)
     st = lib.pa_prefill_q8(
-        *p[:8], qs, scale, ctypes.byref(desc), p[8],
-        workspace.numel() * workspace.element_size(), p[9], _stream(stream))
-    _lib.check(st, "pa_prefill_q8")
+        *p[:8], _ptr(query_start, "query_start", dev, _tc["i32"]), scale,
+        ctypes.byref(desc), p[8], workspace.nbytes, p[9],
+        _stream_on(stream, dev))
+    if st:
+        _lib.check(st, "pa_prefill_q8")
     return out
 
 
@@ -664,17 +703,21 @@ def pa_copy_blocks_q8(k_cache, v_cache, k_scales, v_scales, pairs, *,
                       dev_err=None, stream=None):
     """``pa_copy_blocks`` for the 8-bit cache: codes and scales of block
     pairs[i, 0] into block pairs[i, 1]."""
-    import torch
+    tc = _tc or _torch_refs()
     nb, hkv, bs, d = _check_q8(k_cache, v_cache, k_scales, v_scales)
     if pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError("pairs must be [num_pairs, 2]")
-    e4m3, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
-    p = _on_current((k_cache, "k_cache", e4m3), (v_cache, "v_cache", e4m3),
-                    (k_scales, "k_scales", f32), (v_scales, "v_scales", f32),
-                    (pairs, "pairs", i32), (dev_err, "dev_err", i32))
-    st = _lib.load().pa_copy_blocks_q8(*p[:5], pairs.shape[0], hkv, d, bs, nb,
-                                       p[5], _stream(stream))
-    _lib.check(st, "pa_copy_blocks_q8")
+    e4m3, f32, i32 = tc["e4m3"], tc["f32"], tc["i32"]
+    dev = tc["device"]()
+    st = _lib.load().pa_copy_blocks_q8(
+        _ptr(k_cache, "k_cache", dev, e4m3),
+        _ptr(v_cache, "v_cache", dev, e4m3),
+        _ptr(k_scales, "k_scales", dev, f32),
+        _ptr(v_scales, "v_scales", dev, f32), _ptr(pairs, "pairs", dev, i32),
+        pairs.shape[0], hkv, d, bs, nb, _ptr(dev_err, "dev_err", dev, i32),
+        _stream_on(stream, dev))
+    if st:
+        _lib.check(st, "pa_copy_blocks_q8")
 
 
 def pa_swap_blocks_q8(dst_k, dst_v, dst_k_scales, dst_v_scales, src_k, src_v,

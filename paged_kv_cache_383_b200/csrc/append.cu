@@ -39,6 +39,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxWindow = 16;  // rows whose blocks one K/V CTA looks after
 constexpr int kMaxBlock = 32;   // block_size
 constexpr int kMaxPairs = 64;   // rotated pairs: head_dim / 2
+constexpr int kMaxTokens = 8;   // tokens whose rows one CTA streams
 // Scales written by pa_append_q8: 2^e with e in this range.
 constexpr int kMinScaleExp = -64, kMaxScaleExp = 120;
 
@@ -65,6 +66,7 @@ struct AppendArgs {
   int rot_pairs;  // rot_dim / 2
   int interleaved;
   float rope_scale, norm_eps;
+  int tokens;       // tokens per CTA (1 with row_splits > 1)
   int row_splits;   // CTAs that share a token's rows
   int kv_ctas;      // pa_append_q8: CTAs 0 .. kv_ctas - 1 write K and V
   int window;       // rows per K/V window
@@ -176,97 +178,147 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     dev::Mma<T>::pack(x[6], x[7]));
 }
 
-// Rows that keep 16 bits: the query heads, and (16-bit cache) the key and
-// value heads, of one token; `split` of its row_splits CTAs.
+// Rows that keep 16 bits, the query heads and (16-bit cache) the key and value
+// heads, of tokens t0 .. t0 + a.tokens - 1; `split` of the row_splits CTAs
+// that share them.  What hangs on the chain sequence -> length -> block id
+// and the sines is looked up once for all the tokens, behind the first loads;
+// then the rows stream through, each batch loaded before the one ahead of it
+// is worked on.
 template <typename T, int D, bool kQ8>
-__device__ __forceinline__ void token_rows(const AppendArgs& a, int t,
+__device__ __forceinline__ void token_rows(const AppendArgs& a, int t0,
                                            int split, float2* cs) {
   constexpr int LPR = D / 8;               // lanes per row
   constexpr int kSlots = kThreads / LPR;   // rows per pass of the CTA
-  constexpr int kBatch = 4;                // passes in flight
-  __shared__ int s_b;
+  constexpr int kBatch = 4;                // passes loaded together
+  __shared__ int s_seq[kMaxTokens];
+  __shared__ int s_pos[kMaxTokens];  // -1: no such row, or padding
+  __shared__ int s_blk[kMaxTokens];  // -1: K and V are not written
   const int tid = threadIdx.x;
   const int c = tid % LPR, slot = tid / LPR;
   const int rows = a.num_q_heads + (kQ8 ? 0 : 2 * a.num_kv_heads);
+  const int n_tok = min(a.tokens, a.total_q - t0);
   const int step = kSlots * a.row_splits;
-  const int first = split * kSlots + slot;
-  // Element 8c of row r of this token.
-  auto src = [&](int r) -> const uint4* {
+  // A row of this CTA: token i, row r of it.
+  struct Row {
+    int i, r;
+  };
+  auto advance = [&](Row& w) {
+    w.r += step;
+    while (w.r >= rows && w.i < n_tok) {
+      w.r -= rows;
+      ++w.i;
+    }
+  };
+  auto src = [&](const Row& w) -> const uint4* {
+    const int64_t t = t0 + w.i;
     const T* p;
-    if (r < a.num_q_heads)
-      p = static_cast<const T*>(a.q) + t * a.q_stride + r * D;
-    else if (r < a.num_q_heads + a.num_kv_heads)
+    if (w.r < a.num_q_heads)
+      p = static_cast<const T*>(a.q) + t * a.q_stride + w.r * D;
+    else if (w.r < a.num_q_heads + a.num_kv_heads)
       p = static_cast<const T*>(a.k) + t * a.k_stride +
-          (r - a.num_q_heads) * D;
+          (w.r - a.num_q_heads) * D;
     else
       p = static_cast<const T*>(a.v) + t * a.v_stride +
-          (r - a.num_q_heads - a.num_kv_heads) * D;
+          (w.r - a.num_q_heads - a.num_kv_heads) * D;
     return reinterpret_cast<const uint4*>(p) + c;
   };
-  uint4 raw[kBatch];
-#pragma unroll
-  for (int u = 0; u < kBatch; ++u)
-    if (first + u * step < rows) raw[u] = *src(first + u * step);
-
-  int b = t;
-  if (a.query_start) {
-    if (tid == 0) s_b = -1;
-    __syncthreads();
-    for (int j = tid; j < a.num_seqs; j += kThreads)
-      if (a.query_start[j] <= t && t < a.query_start[j + 1]) s_b = j;
-    __syncthreads();
-    b = s_b;
-    if (b < 0) return;  // a row behind the last sequence: left as it was
-  }
-  const Seq sq = read_seq(a, b);
-  if (!sq.ok) return;
-  const int pos = sq.L - sq.q_len + t - sq.q0;
-  int blk = 0;
-  if constexpr (!kQ8) {
-    blk = a.block_tables[static_cast<int64_t>(b) * a.max_blocks_per_seq +
-                         pos / a.block_size];
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (tid == 0) dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
-      blk = -1;
-    }
-  }
-  if (tid < a.rot_pairs) cs[tid] = turn(a, tid, pos);
-  __syncthreads();
-
-  const int64_t page = static_cast<int64_t>(blk) * a.num_kv_heads;
-  for (int r0 = first; r0 - slot < rows; r0 += kBatch * step) {
-    if (r0 != first) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (r0 + u * step < rows) raw[u] = *src(r0 + u * step);
-    }
+  Row w{0, split * kSlots + slot - step};
+  advance(w);
+  auto load = [&](Row& first, uint4 (&raw)[kBatch]) {
+    first = w;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int r = r0 + u * step;
-      if (r - slot >= rows) break;  // uniform over the CTA
+      if (w.i < n_tok) raw[u] = *src(w);
+      advance(w);
+    }
+  };
+  Row at;
+  uint4 raw[kBatch];
+  load(at, raw);
+
+  if (tid < kMaxTokens) {
+    s_seq[tid] = a.query_start ? -1 : t0 + tid;
+  }
+  if (a.query_start) {
+    __syncthreads();
+    for (int j = tid; j < a.num_seqs; j += kThreads) {
+      const int lo = max(a.query_start[j], t0);
+      const int hi = min(a.query_start[j + 1], t0 + n_tok);
+      for (int t = lo; t < hi; ++t) s_seq[t - t0] = j;
+    }
+  }
+  __syncthreads();
+  if (tid < n_tok) {
+    const int b = s_seq[tid];
+    int pos = -1, blk = -1;
+    if (b >= 0) {  // else a row behind the last sequence
+      const Seq sq = read_seq(a, b);
+      if (sq.ok) {
+        pos = sq.L - sq.q_len + t0 + tid - sq.q0;
+        if constexpr (!kQ8) {
+          blk = a.block_tables[static_cast<int64_t>(b) *
+                                   a.max_blocks_per_seq +
+                               pos / a.block_size];
+          if (blk < 0 || blk >= a.num_blocks) {
+            dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
+            blk = -1;
+          }
+        }
+      }
+    }
+    s_pos[tid] = pos;
+    s_blk[tid] = blk;
+  }
+  __syncthreads();
+  for (int j = tid; j < n_tok * a.rot_pairs; j += kThreads) {
+    const int i = j / a.rot_pairs;
+    if (s_pos[i] >= 0) cs[j] = turn(a, j - i * a.rot_pairs, s_pos[i]);
+  }
+  __syncthreads();
+
+  // Passes of the whole CTA (every thread takes part in the shuffles).
+  const int passes = (n_tok * rows + step - 1) / step;
+  for (int p0 = 0; p0 < passes; p0 += kBatch) {
+    Row next;
+    uint4 ahead[kBatch];
+    load(next, ahead);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (p0 + u >= passes) break;
+      const bool live = at.i < n_tok;
+      const int r = at.r;
+      const int pos = live ? s_pos[at.i] : -1;
       const bool is_q = r < a.num_q_heads;
       const int kv = r - a.num_q_heads;  // key heads, then value heads
       const bool is_v = kv >= a.num_kv_heads;
       float x[8] = {};
-      if (r < rows) unpack8<T>(raw[u], x);
+      if (live) unpack8<T>(raw[u], x);
       norm_rotate<T, D>(x,
                         static_cast<const T*>(is_q ? a.q_norm
                                               : is_v ? nullptr : a.k_norm),
-                        is_q || !is_v, cs, a, c);
-      if (r >= rows) continue;
-      T* dst;
-      if (is_q) {
-        dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + r * D;
-      } else {
-        if (blk < 0) continue;
-        const int h = is_v ? kv - a.num_kv_heads : kv;
-        dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) +
-              ((page + h) * a.block_size + pos % a.block_size) * D;
+                        is_q || !is_v, cs + (live ? at.i : 0) * a.rot_pairs,
+                        a, c);
+      if (pos >= 0) {
+        T* dst = nullptr;
+        if (is_q) {
+          dst = static_cast<T*>(a.q_out) + (t0 + at.i) * a.q_out_stride +
+                r * D;
+        } else if (s_blk[at.i] >= 0) {
+          const int h = is_v ? kv - a.num_kv_heads : kv;
+          dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) +
+                ((static_cast<int64_t>(s_blk[at.i]) * a.num_kv_heads + h) *
+                     a.block_size + pos % a.block_size) * D;
+        }
+        // V unchanged: the very bits (a NaN's payload too).
+        if (dst)
+          reinterpret_cast<uint4*>(dst)[c] =
+              !is_q && is_v ? raw[u] : pack8<T>(x);
       }
-      // V unchanged: the very bits (a NaN's payload too).
-      reinterpret_cast<uint4*>(dst)[c] =
-          !is_q && is_v ? raw[u] : pack8<T>(x);
+      advance(at);
     }
+    at = next;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) raw[u] = ahead[u];
   }
 }
 
@@ -287,7 +339,7 @@ __device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
                                               int h, int row, int n, int blk,
                                               int o, const float2* cs) {
   constexpr int LPR = D / 8, kRows = 32 / LPR;  // rows per pass
-  constexpr int kKeep = 4;                      // passes held in registers
+  constexpr int kKeep = 8;                      // passes held in registers
   const int lane = threadIdx.x & 31;
   const int c = lane % LPR, sub = lane / LPR;
   const T* base = is_k ? static_cast<const T*>(a.k) + row * a.k_stride
@@ -310,22 +362,23 @@ __device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
                         cs + min(r, n - 1) * a.rot_pairs, a, c);
   };
   float amax = 0.f;
-  float kept[kKeep][8];
   const int passes = (n + kRows - 1) / kRows;
-  // Up to kKeep passes stay in registers; longer runs (a whole block of a
-  // prompt) are read and rotated twice, the second time from L1: holding 32
-  // rows of 128 would take 128 registers a lane.
+  // Up to kKeep passes stay in registers as they were read; longer runs (a
+  // block of 32 at head_dim 128) are read again for their codes, from L1 or
+  // L2.  Norm and rotation are done twice either way: keeping their fp32
+  // results would take twice the registers.
+  uint4 raw[kKeep];
   for (int p0 = 0; p0 < passes; p0 += kKeep) {
-    uint4 raw[kKeep];
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) raw[u] = load((p0 + u) * kRows + sub);
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
       if (p0 + u >= passes) break;
-      value(raw[u], (p0 + u) * kRows + sub, kept[u]);
+      float x[8];
+      value(raw[u], (p0 + u) * kRows + sub, x);
       if ((p0 + u) * kRows + sub < n)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(kept[u][e]));
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
     }
   }
 #pragma unroll
@@ -367,19 +420,15 @@ __device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
   };
   for (int p0 = 0; p0 < passes; p0 += kKeep) {
     if (passes > kKeep) {
-      uint4 raw[kKeep];
 #pragma unroll
       for (int u = 0; u < kKeep; ++u) raw[u] = load((p0 + u) * kRows + sub);
-#pragma unroll
-      for (int u = 0; u < kKeep; ++u) {
-        if (p0 + u >= passes) break;
-        value(raw[u], (p0 + u) * kRows + sub, kept[u]);
-      }
     }
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
       if (p0 + u >= passes) break;
-      store(kept[u], (p0 + u) * kRows + sub);
+      float x[8];
+      value(raw[u], (p0 + u) * kRows + sub, x);
+      store(x, (p0 + u) * kRows + sub);
     }
   }
 }
@@ -461,8 +510,8 @@ __device__ __forceinline__ void window_kv(const AppendArgs& a, int w,
 template <typename T, int D, bool kQ8>
 __global__ void __launch_bounds__(kThreads)
     append_kernel(const AppendArgs a) {
-  // cos/sin: one token's pairs, or those of a block's tokens.
-  __shared__ float2 cs[kQ8 ? kMaxBlock * (D / 2) : kMaxPairs];
+  // cos/sin: the pairs of the CTA's tokens, or of a block's.
+  __shared__ float2 cs[kQ8 ? kMaxBlock * (D / 2) : kMaxTokens * kMaxPairs];
   dev::pdl_trigger();  // a following attention may run its prologue now
   dev::pdl_wait();     // q, k and v may be the previous kernel's output
   if (kQ8 && static_cast<int>(blockIdx.x) < a.kv_ctas) {
@@ -470,7 +519,8 @@ __global__ void __launch_bounds__(kThreads)
                     cs);
   } else {
     const unsigned i = blockIdx.x - (kQ8 ? a.kv_ctas : 0);
-    token_rows<T, D, kQ8>(a, i / a.row_splits, i % a.row_splits, cs);
+    token_rows<T, D, kQ8>(a, static_cast<int>(i / a.row_splits) * a.tokens,
+                          i % a.row_splits, cs);
   }
 }
 
@@ -607,16 +657,20 @@ pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
   a.interleaved = d->rope_layout == PA_ROPE_INTERLEAVED;
   a.rope_scale = d->rope_scale;
   a.norm_eps = d->norm_eps;
-  // Rows of one token: one CTA takes them in passes of 16 (head_dim 128) or
-  // 32; with few tokens its passes are dealt out to several CTAs, as long as
-  // the grid stays within about four CTAs per SM.
+  // Rows of one token: a CTA takes them in passes of 16 (head_dim 128) or 32.
+  // With few tokens the passes are dealt out to several CTAs, as long as the
+  // grid stays within about four CTAs per SM; with many a CTA streams up to
+  // eight tokens, as long as it leaves that many.
   const int slots = kThreads / (d->head_dim / 8);
   const int rows = d->num_q_heads + (kQ8 ? 0 : 2 * d->num_kv_heads);
   const int passes = (rows + slots - 1) / slots;
   const int64_t room = 4LL * device_sm_count();
   a.row_splits = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(passes, room / d->total_q)));
-  int64_t ctas = static_cast<int64_t>(d->total_q) * a.row_splits;
+  a.tokens = static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>(kMaxTokens, d->total_q / room)));
+  int64_t ctas = (static_cast<int64_t>(d->total_q) + a.tokens - 1) /
+                 a.tokens * a.row_splits;
   if (rows == 0) ctas = 0;
   a.kv_ctas = 0;
   a.window = 1;

@@ -568,12 +568,16 @@ pa_status launch_q8(const pa_decode_desc* d, const DecodeArgs& a,
   auto kern = decode_q8_kernel<T, BS, D, S>;
   const size_t smem = smem_bytes_q8<BS, D, S>(
       (a.warp_parts ? kConsumers : 1) * a.partition_size / BS);
-  const cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(smem_bytes_q8<BS, D, S>(kMaxPartition / BS)));
-  if (e != cudaSuccess)
-    return fail(PA_ERR_CUDA, "pa_decode_q8: cudaFuncSetAttribute: %s",
-                cudaGetErrorString(e));
+  static OncePerDevice configured;
+  if (configured.needed()) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>(smem_bytes_q8<BS, D, S>(kMaxPartition / BS)));
+    if (e != cudaSuccess)
+      return fail(PA_ERR_CUDA, "pa_decode_q8: cudaFuncSetAttribute: %s",
+                  cudaGetErrorString(e));
+    configured.mark();
+  }
   return launch_chain<T, D, BS>(
       "pa_decode_q8", d, a, smem, stream, [&](const cudaLaunchConfig_t& cfg) {
         return cudaLaunchKernelEx(&cfg, kern, km, vm, a, sc);

@@ -951,18 +951,24 @@ template <typename T, int BS, int G, int D>
 pa_status launch(const PrefillQ8Args& a, cudaStream_t st) {
   auto kern = prefill_q8_kernel<T, BS, G, D>;
   const size_t smem = LayoutQ8<D>::kSmemBytes;
-  // The warpgroups' shares of the registers assume kLaunchRegs a thread.
-  cudaFuncAttributes attrs;
-  cudaError_t e = cudaFuncGetAttributes(&attrs, kern);
-  if (e != cudaSuccess || attrs.numRegs != kLaunchRegs)
-    return fail(PA_ERR_CUDA, "pa_prefill_q8: built with %d registers, not %d",
-                e == cudaSuccess ? attrs.numRegs : -1, kLaunchRegs);
-  e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(smem));
-  if (e != cudaSuccess)
-    return fail(PA_ERR_CUDA, "pa_prefill_q8: cudaFuncSetAttribute(%zu): %s",
-                smem, cudaGetErrorString(e));
+  static OncePerDevice configured;
+  cudaError_t e = cudaSuccess;
+  if (configured.needed()) {
+    // The warpgroups' shares of the registers assume kLaunchRegs a thread.
+    cudaFuncAttributes attrs;
+    e = cudaFuncGetAttributes(&attrs, kern);
+    if (e != cudaSuccess || attrs.numRegs != kLaunchRegs)
+      return fail(PA_ERR_CUDA,
+                  "pa_prefill_q8: built with %d registers, not %d",
+                  e == cudaSuccess ? attrs.numRegs : -1, kLaunchRegs);
+    e = cudaFuncSetAttribute(
+        kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>(smem));
+    if (e != cudaSuccess)
+      return fail(PA_ERR_CUDA, "pa_prefill_q8: cudaFuncSetAttribute(%zu): %s",
+                  smem, cudaGetErrorString(e));
+    configured.mark();
+  }
   cudaLaunchConfig_t cfg = {};
   const int64_t slots = std::max(device_sm_count(), 1);  // one CTA per SM
   cfg.gridDim =

@@ -3,7 +3,9 @@
 #pragma once
 
 #include <cudaTypedefs.h>
+#include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdint>
 
@@ -27,6 +29,23 @@ int device_sm_count();
 
 // The driver's cuTensorMapEncodeTiled, or nullptr if it is unavailable.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// Which devices a kernel's attributes were set on: a static one of these
+// beside a launch spares the runtime calls on every later one.
+struct OncePerDevice {
+  std::atomic<uint64_t> mask{0};
+  // True if not yet marked for the current device.
+  bool needed() const {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return true;
+    return !(mask.load(std::memory_order_acquire) >> dev & 1u);
+  }
+  void mark() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64)
+      mask.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  }
+};
 
 // Address at which the current device reaches `p`: device memory of this
 // device, or mapped page-locked host memory.  nullptr for anything else
