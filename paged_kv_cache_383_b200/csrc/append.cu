@@ -107,7 +107,7 @@ __device__ __forceinline__ float2 turn(const AppendArgs& a, int pair, int p) {
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -117,62 +117,88 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   }
 }
 
-// Norm (weight non-null) and rotation of a head row spread over LPR lanes,
-// lane c of them holding elements 8c .. 8c + 7.  cs: the row's cos/sin pairs
-// in shared memory.  rotate / weight may differ between a warp's rows; every
-// lane takes part in the shuffles.
+// A head row is spread over D / 16 lanes; a lane holds two chunks of eight
+// elements (16 bytes).  With h = rot_dim / 16 lanes' worth of rotated pairs,
+// lane l < h holds both sides of pairs 8l .. 8l + 7: chunks l and l + h in the
+// half layout, 2l and 2l + 1 in the interleaved one; the lanes past them hold
+// chunks 2l and 2l + 1, which do not turn.  So the rotation needs no other
+// lane, and its eight sines serve the lane for every head of a token.
+struct Chunks {
+  int a, b;
+  bool turns;
+};
+__device__ __forceinline__ Chunks chunks_of(const AppendArgs& a, int l) {
+  const int h = a.rot_pairs / 8;
+  const bool apart = l < h && !a.interleaved;
+  return Chunks{apart ? l : 2 * l, apart ? l + h : 2 * l + 1, l < h};
+}
+
+// Shared memory holds a token's pairs in groups of eight, 80 bytes apart: the
+// eight lanes of a 16-byte load phase then read all 32 banks.
+constexpr int kGroupStride = 10;  // float2
+__device__ __forceinline__ int pair_at(int pair) {
+  return (pair >> 3) * kGroupStride + (pair & 7);
+}
+constexpr int kTokenStride = kMaxPairs / 8 * kGroupStride;  // float2 per token
+
+// Norm (weight non-null) and rotation (turn) of a head row; x[0 .. 7] is this
+// lane's chunk ch.a, x[8 .. 15] its chunk ch.b, z its pairs' cos and sin.
+// Every lane takes part in the shuffles.
 template <typename T, int D>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], const T* weight,
-                                            bool rotate, const float2* cs,
-                                            const AppendArgs& a, int c) {
-  constexpr int LPR = D / 8;
+__device__ __forceinline__ void norm_rotate(float (&x)[16], const T* weight,
+                                            bool turn, const float2 (&z)[8],
+                                            const AppendArgs& a,
+                                            const Chunks& ch) {
   if (a.q_norm || a.k_norm) {  // uniform over the grid
     float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-    for (int m = 1; m < LPR; m <<= 1)
+    for (int m = 1; m < D / 16; m <<= 1)
       ss += __shfl_xor_sync(0xffffffffu, ss, m);
     if (weight) {
       const float r = rsqrtf(ss * (1.f / D) + a.norm_eps);
       float w[8];
-      unpack8<T>(reinterpret_cast<const uint4*>(weight)[c], w);
+      unpack8<T>(reinterpret_cast<const uint4*>(weight)[ch.a], w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+      unpack8<T>(reinterpret_cast<const uint4*>(weight)[ch.b], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[8 + e] = x[8 + e] * r * w[e];
     }
   }
-  if (a.rot_pairs == 0) return;
-  const int lane = threadIdx.x & 31;
+  if (!turn) return;
   if (a.interleaved) {
-    if (rotate && 4 * c < a.rot_pairs) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 z = cs[4 * c + i];
-        const float u = x[2 * i], w = x[2 * i + 1];
-        x[2 * i] = u * z.x - w * z.y;
-        x[2 * i + 1] = w * z.x + u * z.y;
-      }
+    for (int e = 0; e < 8; ++e) {
+      const float u = x[2 * e], w = x[2 * e + 1];
+      x[2 * e] = u * z[e].x - w * z[e].y;
+      x[2 * e + 1] = w * z[e].x + u * z[e].y;
     }
   } else {
-    // Chunk c's partners are chunk c +- rot_pairs / 8, in another lane.
-    const int half = a.rot_pairs / 8;
-    const bool in = c < 2 * half, second = c >= half;
-    const int src = in ? (second ? lane - half : lane + half) : lane;
-    float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      y[e] = __shfl_sync(0xffffffffu, x[e], src);
-    if (rotate && in) {
-      const float2* z = cs + 8 * (second ? c - half : c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = x[e] * z[e].x + (second ? y[e] : -y[e]) * z[e].y;
+    for (int e = 0; e < 8; ++e) {
+      const float u = x[e], w = x[8 + e];
+      x[e] = u * z[e].x - w * z[e].y;
+      x[8 + e] = w * z[e].x + u * z[e].y;
     }
   }
 }
 
+__device__ __forceinline__ void load_pairs(const float2* cs, int l,
+                                           float2 (&z)[8]) {
+  const float4* from =
+      reinterpret_cast<const float4*>(cs + l * kGroupStride);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float4 v = from[e];
+    z[2 * e] = make_float2(v.x, v.y);
+    z[2 * e + 1] = make_float2(v.z, v.w);
+  }
+}
+
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(dev::Mma<T>::pack(x[0], x[1]), dev::Mma<T>::pack(x[2], x[3]),
                     dev::Mma<T>::pack(x[4], x[5]),
                     dev::Mma<T>::pack(x[6], x[7]));
@@ -182,19 +208,19 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // heads, of tokens t0 .. t0 + a.tokens - 1; `split` of the row_splits CTAs
 // that share them.  What hangs on the chain sequence -> length -> block id
 // and the sines is looked up once for all the tokens, behind the first loads;
-// then the rows stream through, each batch loaded before the one ahead of it
-// is worked on.
+// then the rows stream through.
 template <typename T, int D, bool kQ8>
 __device__ __forceinline__ void token_rows(const AppendArgs& a, int t0,
                                            int split, float2* cs) {
-  constexpr int LPR = D / 8;               // lanes per row
+  constexpr int LPR = D / 16;              // lanes per row
   constexpr int kSlots = kThreads / LPR;   // rows per pass of the CTA
-  constexpr int kBatch = 4;                // passes loaded together
+  constexpr int kBatch = 2;                // passes loaded together
   __shared__ int s_seq[kMaxTokens];
   __shared__ int s_pos[kMaxTokens];  // -1: no such row, or padding
   __shared__ int s_blk[kMaxTokens];  // -1: K and V are not written
   const int tid = threadIdx.x;
-  const int c = tid % LPR, slot = tid / LPR;
+  const int l = tid % LPR, slot = tid / LPR;
+  const Chunks ch = chunks_of(a, l);
   const int rows = a.num_q_heads + (kQ8 ? 0 : 2 * a.num_kv_heads);
   const int n_tok = min(a.tokens, a.total_q - t0);
   const int step = kSlots * a.row_splits;
@@ -220,20 +246,24 @@ __device__ __forceinline__ void token_rows(const AppendArgs& a, int t0,
     else
       p = static_cast<const T*>(a.v) + t * a.v_stride +
           (w.r - a.num_q_heads - a.num_kv_heads) * D;
-    return reinterpret_cast<const uint4*>(p) + c;
+    return reinterpret_cast<const uint4*>(p);
   };
   Row w{0, split * kSlots + slot - step};
   advance(w);
-  auto load = [&](Row& first, uint4 (&raw)[kBatch]) {
+  auto load = [&](Row& first, uint4 (&raw)[kBatch][2]) {
     first = w;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (w.i < n_tok) raw[u] = *src(w);
+      if (w.i < n_tok) {
+        const uint4* p = src(w);
+        raw[u][0] = p[ch.a];
+        raw[u][1] = p[ch.b];
+      }
       advance(w);
     }
   };
   Row at;
-  uint4 raw[kBatch];
+  uint4 raw[kBatch][2];
   load(at, raw);
 
   if (tid < kMaxTokens) {
@@ -272,16 +302,18 @@ __device__ __forceinline__ void token_rows(const AppendArgs& a, int t0,
   __syncthreads();
   for (int j = tid; j < n_tok * a.rot_pairs; j += kThreads) {
     const int i = j / a.rot_pairs;
-    if (s_pos[i] >= 0) cs[j] = turn(a, j - i * a.rot_pairs, s_pos[i]);
+    const int pair = j - i * a.rot_pairs;
+    if (s_pos[i] >= 0)
+      cs[i * kTokenStride + pair_at(pair)] = turn(a, pair, s_pos[i]);
   }
   __syncthreads();
 
   // Passes of the whole CTA (every thread takes part in the shuffles).
   const int passes = (n_tok * rows + step - 1) / step;
+  int z_tok = -1;  // whose pairs are in z
+  float2 z[8];
   for (int p0 = 0; p0 < passes; p0 += kBatch) {
-    Row next;
-    uint4 ahead[kBatch];
-    load(next, ahead);
+    if (p0 > 0) load(at, raw);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (p0 + u >= passes) break;
@@ -291,13 +323,19 @@ __device__ __forceinline__ void token_rows(const AppendArgs& a, int t0,
       const bool is_q = r < a.num_q_heads;
       const int kv = r - a.num_q_heads;  // key heads, then value heads
       const bool is_v = kv >= a.num_kv_heads;
-      float x[8] = {};
-      if (live) unpack8<T>(raw[u], x);
+      float x[16] = {};
+      if (live) {
+        unpack8<T>(raw[u][0], x);
+        unpack8<T>(raw[u][1], x + 8);
+        if (z_tok != at.i && ch.turns) {
+          load_pairs(cs + at.i * kTokenStride, l, z);
+          z_tok = at.i;
+        }
+      }
       norm_rotate<T, D>(x,
                         static_cast<const T*>(is_q ? a.q_norm
                                               : is_v ? nullptr : a.k_norm),
-                        is_q || !is_v, cs + (live ? at.i : 0) * a.rot_pairs,
-                        a, c);
+                        ch.turns && (is_q || !is_v), z, a, ch);
       if (pos >= 0) {
         T* dst = nullptr;
         if (is_q) {
@@ -309,16 +347,17 @@ __device__ __forceinline__ void token_rows(const AppendArgs& a, int t0,
                 ((static_cast<int64_t>(s_blk[at.i]) * a.num_kv_heads + h) *
                      a.block_size + pos % a.block_size) * D;
         }
-        // V unchanged: the very bits (a NaN's payload too).
-        if (dst)
-          reinterpret_cast<uint4*>(dst)[c] =
-              !is_q && is_v ? raw[u] : pack8<T>(x);
+        if (dst) {
+          // V unchanged: the very bits (a NaN's payload too).
+          const bool copy = !is_q && is_v;
+          reinterpret_cast<uint4*>(dst)[ch.a] =
+              copy ? raw[u][0] : pack8<T>(x);
+          reinterpret_cast<uint4*>(dst)[ch.b] =
+              copy ? raw[u][1] : pack8<T>(x + 8);
+        }
       }
       advance(at);
     }
-    at = next;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) raw[u] = ahead[u];
   }
 }
 
@@ -338,10 +377,11 @@ template <typename T, int D>
 __device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
                                               int h, int row, int n, int blk,
                                               int o, const float2* cs) {
-  constexpr int LPR = D / 8, kRows = 32 / LPR;  // rows per pass
-  constexpr int kKeep = 8;                      // passes held in registers
+  constexpr int LPR = D / 16, kRows = 32 / LPR;  // rows per pass
+  constexpr int kKeep = 4;                       // passes held in registers
   const int lane = threadIdx.x & 31;
-  const int c = lane % LPR, sub = lane / LPR;
+  const int l = lane % LPR, sub = lane / LPR;
+  const Chunks ch = chunks_of(a, l);
   const T* base = is_k ? static_cast<const T*>(a.k) + row * a.k_stride
                        : static_cast<const T*>(a.v) + row * a.v_stride;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
@@ -351,15 +391,25 @@ __device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
   const float s_old = o > 0 ? *sp : 0.f;
   uint8_t* page = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) +
                   unit * a.block_size * D;
-  auto load = [&](int r) {
-    return r < n ? reinterpret_cast<const uint4*>(base + r * stride + h * D)[c]
-                 : make_uint4(0u, 0u, 0u, 0u);
+  uint4 raw[kKeep][2];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+      const int r = (p0 + u) * kRows + sub;
+      const uint4* p =
+          reinterpret_cast<const uint4*>(base + r * stride + h * D);
+      raw[u][0] = r < n ? p[ch.a] : make_uint4(0u, 0u, 0u, 0u);
+      raw[u][1] = r < n ? p[ch.b] : make_uint4(0u, 0u, 0u, 0u);
+    }
   };
-  auto value = [&](const uint4& raw, int r, float (&x)[8]) {
-    unpack8<T>(raw, x);
-    if (is_k)  // uniform over the warp
-      norm_rotate<T, D>(x, weight, true,
-                        cs + min(r, n - 1) * a.rot_pairs, a, c);
+  auto value = [&](int u, int r, float (&x)[16]) {
+    unpack8<T>(raw[u][0], x);
+    unpack8<T>(raw[u][1], x + 8);
+    if (is_k) {  // uniform over the warp
+      float2 z[8];
+      if (ch.turns) load_pairs(cs + min(r, n - 1) * kTokenStride, l, z);
+      norm_rotate<T, D>(x, weight, ch.turns, z, a, ch);
+    }
   };
   float amax = 0.f;
   const int passes = (n + kRows - 1) / kRows;
@@ -367,18 +417,16 @@ __device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
   // block of 32 at head_dim 128) are read again for their codes, from L1 or
   // L2.  Norm and rotation are done twice either way: keeping their fp32
   // results would take twice the registers.
-  uint4 raw[kKeep];
   for (int p0 = 0; p0 < passes; p0 += kKeep) {
-#pragma unroll
-    for (int u = 0; u < kKeep; ++u) raw[u] = load((p0 + u) * kRows + sub);
+    load(p0);
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
       if (p0 + u >= passes) break;
-      float x[8];
-      value(raw[u], (p0 + u) * kRows + sub, x);
+      float x[16];
+      value(u, (p0 + u) * kRows + sub, x);
       if ((p0 + u) * kRows + sub < n)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
     }
   }
 #pragma unroll
@@ -409,25 +457,26 @@ __device__ __forceinline__ void quantise_unit(const AppendArgs& a, bool is_k,
   // x / s; times the reciprocal where that is exact (a power of two).
   const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0u;
   const float inv = 1.f / s;
-  auto store = [&](const float (&x)[8], int r) {
+  auto store = [&](const float (&x)[16], int r) {
     if (r >= n) return;
-    float y[8];
+    float y[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = pow2 ? x[e] * inv : x[e] / s;
-    *reinterpret_cast<uint2*>(page + static_cast<int64_t>(o + r) * D + 8 * c) =
+    for (int e = 0; e < 16; ++e) y[e] = pow2 ? x[e] * inv : x[e] / s;
+    uint8_t* to = page + static_cast<int64_t>(o + r) * D;
+    *reinterpret_cast<uint2*>(to + 8 * ch.a) =
         make_uint2(dev::f32x4_to_e4m3x4(y[0], y[1], y[2], y[3]),
                    dev::f32x4_to_e4m3x4(y[4], y[5], y[6], y[7]));
+    *reinterpret_cast<uint2*>(to + 8 * ch.b) =
+        make_uint2(dev::f32x4_to_e4m3x4(y[8], y[9], y[10], y[11]),
+                   dev::f32x4_to_e4m3x4(y[12], y[13], y[14], y[15]));
   };
   for (int p0 = 0; p0 < passes; p0 += kKeep) {
-    if (passes > kKeep) {
-#pragma unroll
-      for (int u = 0; u < kKeep; ++u) raw[u] = load((p0 + u) * kRows + sub);
-    }
+    if (passes > kKeep) load(p0);
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
       if (p0 + u >= passes) break;
-      float x[8];
-      value(raw[u], (p0 + u) * kRows + sub, x);
+      float x[16];
+      value(u, (p0 + u) * kRows + sub, x);
       store(x, (p0 + u) * kRows + sub);
     }
   }
@@ -495,7 +544,8 @@ __device__ __forceinline__ void window_kv(const AppendArgs& a, int w,
       __syncthreads();  // the previous run's sines are read
       for (int j = tid; j < n * a.rot_pairs; j += kThreads) {
         const int r = j / a.rot_pairs;
-        cs[j] = turn(a, j - r * a.rot_pairs, pos + r);
+        const int pair = j - r * a.rot_pairs;
+        cs[r * kTokenStride + pair_at(pair)] = turn(a, pair, pos + r);
       }
       __syncthreads();
     }
@@ -508,10 +558,11 @@ __device__ __forceinline__ void window_kv(const AppendArgs& a, int w,
 }
 
 template <typename T, int D, bool kQ8>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     append_kernel(const AppendArgs a) {
   // cos/sin: the pairs of the CTA's tokens, or of a block's.
-  __shared__ float2 cs[kQ8 ? kMaxBlock * (D / 2) : kMaxTokens * kMaxPairs];
+  __shared__ __align__(16) float2
+      cs[(kQ8 ? kMaxBlock : kMaxTokens) * kTokenStride];
   dev::pdl_trigger();  // a following attention may run its prologue now
   dev::pdl_wait();     // q, k and v may be the previous kernel's output
   if (kQ8 && static_cast<int>(blockIdx.x) < a.kv_ctas) {
@@ -657,11 +708,11 @@ pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
   a.interleaved = d->rope_layout == PA_ROPE_INTERLEAVED;
   a.rope_scale = d->rope_scale;
   a.norm_eps = d->norm_eps;
-  // Rows of one token: a CTA takes them in passes of 16 (head_dim 128) or 32.
+  // Rows of one token: a CTA takes them in passes of 32 (head_dim 128) or 64.
   // With few tokens the passes are dealt out to several CTAs, as long as the
   // grid stays within about four CTAs per SM; with many a CTA streams up to
   // eight tokens, as long as it leaves that many.
-  const int slots = kThreads / (d->head_dim / 8);
+  const int slots = kThreads / (d->head_dim / 16);
   const int rows = d->num_q_heads + (kQ8 ? 0 : 2 * d->num_kv_heads);
   const int passes = (rows + slots - 1) / slots;
   const int64_t room = 4LL * device_sm_count();
