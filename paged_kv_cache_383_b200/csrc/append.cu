@@ -39,7 +39,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxWindow = 16;  // rows whose blocks one K/V CTA looks after
 constexpr int kMaxBlock = 32;   // block_size
 constexpr int kMaxPairs = 64;   // rotated pairs: head_dim / 2
-constexpr int kMaxTokens = 8;   // tokens whose rows one CTA streams
+constexpr int kMaxTokens = 4;   // tokens whose rows one CTA streams
 // Scales written by pa_append_q8: 2^e with e in this range.
 constexpr int kMinScaleExp = -64, kMaxScaleExp = 120;
 
@@ -557,8 +557,13 @@ __device__ __forceinline__ void window_kv(const AppendArgs& a, int w,
   }
 }
 
+// Four CTAs per SM (three for the 8-bit cache's kernel, which needs more
+// registers): loads in flight carry the bandwidth (7728 rows of 80 heads 88 us
+// with three, 77 us with four).  K/V CTAs come first: they are the longer
+// chains (spread among the others they ended the grid: 7322 prompt rows 75 us
+// instead of 59).
 template <typename T, int D, bool kQ8>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kQ8 ? 3 : 4)
     append_kernel(const AppendArgs a) {
   // cos/sin: the pairs of the CTA's tokens, or of a block's.
   __shared__ __align__(16) float2
@@ -711,7 +716,7 @@ pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
   // Rows of one token: a CTA takes them in passes of 32 (head_dim 128) or 64.
   // With few tokens the passes are dealt out to several CTAs, as long as the
   // grid stays within about four CTAs per SM; with many a CTA streams up to
-  // eight tokens, as long as it leaves that many.
+  // four tokens, as long as it leaves that many.
   const int slots = kThreads / (d->head_dim / 16);
   const int rows = d->num_q_heads + (kQ8 ? 0 : 2 * d->num_kv_heads);
   const int passes = (rows + slots - 1) / slots;

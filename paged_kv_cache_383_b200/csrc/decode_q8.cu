@@ -82,13 +82,23 @@ constexpr size_t smem_bytes_q8(int pages) {
          ((static_cast<size_t>(pages) * 12 + 15) & ~size_t(15));
 }
 
+// CTAs per SM and the ring of one.  The consumers' work per byte is twice the
+// 16-bit cache's, so warps matter more than bytes in flight: blocks of 16 run
+// five CTAs of 32 KB (batch 256 at 486k tokens: 185 us with three of 64 KB,
+// 176 with four of 48, 172 with five of 32).  Blocks of 32 hold two slices of
+// scores and need the registers of three CTAs; with smaller rings or registers
+// they lose (434k tokens in 8 contexts: 143 us with three of 64 KB, 148 of 48,
+// 163 with registers for four).
+constexpr int ctas_q8(int bs) { return bs == 16 ? 5 : 3; }
+constexpr int ring_bytes_q8(int bs) { return bs == 16 ? 32768 : 65536; }
+
 struct Q8Scales {
   const float* k;  // [num_blocks, num_kv_heads]
   const float* v;
 };
 
 template <typename T, int BS, int D, int S>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, ctas_q8(BS))
     decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
                      const DecodeArgs a, const Q8Scales scales) {
@@ -555,9 +565,9 @@ bool encode_q8_map(CUtensorMap* map, const void* base, uint64_t rows,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 64 KB of ring: three CTAs per SM, whole multiples of the consumer count.
+// Stages in whole multiples of the consumer count.
 constexpr int stages_q8(int bs, int d) {
-  return (65536 / (2 * bs * d)) / kConsumers * kConsumers;
+  return ring_bytes_q8(bs) / (2 * bs * d) / kConsumers * kConsumers;
 }
 
 template <typename T, int BS, int D>
