@@ -57,7 +57,7 @@ namespace {
 constexpr int kKeys = 64;        // keys per K/V tile
 constexpr int kPair = 2;         // query tiles (128 rows each) per work item
 constexpr int kStages = 4;       // fp16 K tiles, and V tiles
-constexpr int kRaw = 4;          // tiles of codes in flight (K and V in turn)
+constexpr int kRaw = 3;          // tiles of codes in flight, of K and of V
 constexpr int kScaleSlots = 16;  // tiles whose scales are staged
 // Warps 0..3 and 4..7: softmax of query tile 0 and 1; 8..11 converters; 12
 // pages and scales; 13 and 14 MMAs of query tile 0 and 1.
@@ -71,8 +71,7 @@ constexpr int kSoftmaxRegs = 192, kConvRegs = 48, kIssueRegs = 80;
 static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs == 4 * kLaunchRegs,
               "more registers than the block was launched with");
 // What the page warp stages for a tile: for each of its blocks ks, the
-// exponent log2(vs) - E + kShift and 2^-that; then the factor of O for a
-// grown E, and E.
+// exponent log2(vs) - E + kShift and 2^-that; and E, last.
 constexpr int kSlotFloats = 16;
 // Tensor memory columns, for each query tile: S 64, P 32, the last 64 dims of
 // q 32, O head_dim (up to 128).
@@ -109,10 +108,10 @@ struct PrefillQ8Args {
   int num_items;
 };
 
-// raw_full[], raw_empty[], k_full[], k_empty[], v_full[], v_empty[]; for each
+// raw_full[], raw_empty[] (of K, then of V), k_full[], k_empty[], v_full[], v_empty[]; for each
 // of the pair q_full, q_empty, s_full, s_free, p_full, o_done; done; item_full[2],
 // item_empty[2].
-constexpr int kNumBars = 2 * kRaw + 4 * kStages + 6 * kPair + 1 + 4;
+constexpr int kNumBars = 4 * kRaw + 4 * kStages + 6 * kPair + 2 + 1 + 4;
 constexpr int kItemWords = 8;
 
 template <int D>
@@ -126,8 +125,10 @@ struct LayoutQ8 {
   static constexpr int kOffK = kOffQ + kPair * kQTile;
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kOffRaw = kOffV + kStages * kTile;
-  static constexpr int kOffScales = kOffRaw + kRaw * kRawTile;
-  static constexpr int kOffBars = kOffScales + kScaleSlots * kSlotFloats * 4;
+  static constexpr int kOffScales = kOffRaw + 2 * kRaw * kRawTile;
+  // maximum, sum and E of each row of query tile 1, for its merge with tile 0
+  static constexpr int kOffMerge = kOffScales + kScaleSlots * kSlotFloats * 4;
+  static constexpr int kOffBars = kOffMerge + 3 * kRows * 4;
   static constexpr size_t kSmemBytes =
       1024 + kOffBars + kNumBars * 8 + 16 + 2 * kItemWords * 4;
 };
@@ -189,7 +190,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
       : "memory");
 }
 
-template <typename T, int BS, int G, int D>
+// kShareKeys: for calls whose items all have at most 128 rows (host rule in
+// launch): the pair of query tiles shares an item's keys (see Span).
+template <typename T, int BS, int G, int D, bool kShareKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q8_kernel(const PrefillQ8Args a) {
   using Lay = LayoutQ8<D>;
@@ -205,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* scale_s = reinterpret_cast<float*>(smem + Lay::kOffScales);
   const uint32_t bars = base + Lay::kOffBars;
   const uint32_t raw_full0 = bars;
-  const uint32_t raw_empty0 = raw_full0 + 8 * kRaw;
-  const uint32_t k_full0 = raw_empty0 + 8 * kRaw;
+  const uint32_t raw_empty0 = raw_full0 + 16 * kRaw;
+  const uint32_t k_full0 = raw_empty0 + 16 * kRaw;
   const uint32_t k_empty0 = k_full0 + 8 * kStages;
   const uint32_t v_full0 = k_empty0 + 8 * kStages;
   const uint32_t v_empty0 = v_full0 + 8 * kStages;
@@ -219,7 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t s_free0 = s_full0 + 8 * kPair;
   const uint32_t p_full0 = s_free0 + 8 * kPair;
   const uint32_t o_done0 = p_full0 + 8 * kPair;
-  const uint32_t done = o_done0 + 8 * kPair;
+  // An item whose keys the pair shares (below): tile 1's part is complete /
+  // has been read.
+  const uint32_t half_done = o_done0 + 8 * kPair;
+  const uint32_t half_read = half_done + 8;
+  const uint32_t done = half_read + 8;
   const uint32_t item_full0 = done + 8;
   const uint32_t item_empty0 = item_full0 + 16;
   uint32_t* tmem_slot =
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   dev::pdl_trigger();
   if (tid == 0) {
-    for (int s = 0; s < kRaw; ++s) {
+    for (int s = 0; s < 2 * kRaw; ++s) {
       dev::mbar_init(raw_full0 + 8 * s, 1);
       dev::mbar_init(raw_empty0 + 8 * s, 4);
     }
@@ -247,6 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::mbar_init(p_full0 + 8 * x, 4);
       dev::mbar_init(o_done0 + 8 * x, 1);
     }
+    dev::mbar_init(half_done, 4);
+    dev::mbar_init(half_read, 4);
     dev::mbar_init(done, 8);
     for (int s = 0; s < 2; ++s) {
       dev::mbar_init(item_full0 + 8 * s, 1);
@@ -270,10 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   constexpr int kWork = 0, kSkip = 1, kEnd = 2;
   // What an item computes: for query tile x new tokens tok0[x] .. + n_q[x] - 1
-  // over n_tiles[x] tiles of keys (0: no such rows); tile 1 has the later
-  // tokens, so n_tiles[1] >= n_tiles[0] or 0.  kv_end: the keys it sees.
+  // over n_tiles[x] tiles of keys; tile 1 has the later tokens, so it sees at
+  // least as many.  kv_end: the keys the item sees, in `tiles` tiles.  With
+  // kShareKeys (a few draft tokens: no tile 1) an item that sees two key tiles
+  // or more has its rows in both query tiles: tile x takes key tiles x, x + 2,
+  // ... (stride 2), and tile 0 merges the two.
   struct Span {
-    int tok0[kPair], n_q[kPair], n_tiles[kPair], kv_end, tiles;
+    int tok0[kPair], n_q[kPair], n_tiles[kPair], kv_end, tiles, stride;
   };
   auto span_of = [](const Item& it) {
     Span sp;
@@ -287,6 +299,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sp.n_q[x] > 0) sp.kv_end = end;
     }
     sp.tiles = max(sp.n_tiles[0], sp.n_tiles[1]);
+    sp.stride = kShareKeys && sp.tiles >= 2 ? 2 : 1;
+    if (sp.stride == 2) {
+      sp.tok0[1] = sp.tok0[0];
+      sp.n_q[1] = sp.n_q[0];
+      sp.n_tiles[0] = (sp.tiles + 1) / 2;
+      sp.n_tiles[1] = sp.tiles / 2;
+    }
     return sp;
   };
   auto read_item = [&](int n, Item& it) -> bool {
@@ -312,28 +331,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kPageWarp) regs_dec<kIssueRegs>();
   if (warp == kPageWarp) {
     // ---------------- work items, pages and scales ----------------
-    // Lane p looks after page p of each tile.
-    const int p = lane;
-    const bool mine = p < kNB;
-    uint32_t u = 0;  // raw tiles of this CTA so far
+    // Lane k looks after page k of a group of 32 / kNB tiles: ids and scales
+    // of a group are read a group ahead (read a tile ahead, their latency
+    // was every tile's period).
+    constexpr int kGroup = 32 / kNB;  // tiles
     uint32_t g = 0;  // K/V tiles of this CTA's earlier items
     bool ok = true;
-    auto acquire = [&]() -> bool {
-      return u < kRaw ||
-             warp_wait(raw_empty0 + 8 * (u % kRaw), ((u / kRaw) - 1) & 1);
-    };
-    auto copy = [&](const uint8_t* cache, int kvh, int32_t id) {
-      const uint32_t full = raw_full0 + 8 * (u % kRaw);
-      __syncwarp();  // the tile's scales, if any, are stored
+    // Tile t (counted over the CTA's items) of K (w = 0) or V (w = 1): its
+    // pages, lane p's own being `id`.
+    auto copy = [&](int w, uint32_t t, const uint8_t* cache, int kvh,
+                    int32_t id) -> bool {
+      const uint32_t slot = w * kRaw + t % kRaw;
+      if (t >= kRaw &&
+          !warp_wait(raw_empty0 + 8 * slot, ((t / kRaw) - 1) & 1))
+        return false;
+      const uint32_t full = raw_full0 + 8 * slot;
       if (lane == 0) dev::mbar_arrive_expect_tx(full, Lay::kRawTile);
       __syncwarp();
-      if (mine)
-        bulk_load(base + Lay::kOffRaw + (u % kRaw) * Lay::kRawTile +
-                      p * BS * D,
+      if (lane < kNB)
+        bulk_load(base + Lay::kOffRaw + slot * Lay::kRawTile + lane * BS * D,
                   cache + (static_cast<int64_t>(id) * a.num_kv_heads + kvh) *
                               (BS * D),
                   BS * D, full);
-      ++u;
+      return true;
     };
     for (int n = 0; ok; ++n) {
       int i = 0;
@@ -387,79 +407,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad_id = false;
       // Pages past the sequence are masked; they read its first page (an
       // invalid id page 0) and take scales that change nothing.
-      auto fetch = [&](int j) -> int32_t {
-        const int page = j * kNB + p;
+      struct Page {
+        int32_t id;
+        float ks, vs;
+      };
+      auto fetch_id = [&](int group) -> int32_t {
+        const int page = group * 32 + lane;
         const int32_t id = __ldg(row + (page < n_pages ? page : 0));
         const bool bad = id < 0 || id >= a.num_blocks;
         bad_id |= bad;
         return bad ? 0 : id;
       };
-      auto fetch_scales = [&](int j, int32_t id) -> float2 {
-        if (j * kNB + p >= n_pages) return make_float2(1.f, 0.f);
+      auto fetch = [&](int group, int32_t id) -> Page {
+        if (group * 32 + lane >= n_pages) return Page{id, 1.f, 0.f};
         const int64_t at = static_cast<int64_t>(id) * a.num_kv_heads + kvh;
-        return make_float2(a.k_scales[at], a.v_scales[at]);
+        return Page{id, a.k_scales[at], a.v_scales[at]};
       };
-      // Ids are read two tiles and scales one tile ahead of their use.
-      int32_t cur = 0, nxt = 0, nn = 0, prv = 0;
-      int e_ref = 0;  // E
-      float2 sc = make_float2(1.f, 0.f), nsc = sc;
-      if (mine) {
-        nxt = fetch(0);
-        if (sp.tiles > 1) nn = fetch(1);
-        nsc = fetch_scales(0, nxt);
-      }
-      for (int t = 0; t <= sp.tiles; ++t) {
+      const int groups = (sp.tiles + kGroup - 1) / kGroup;
+      int32_t id2 = fetch_id(0);  // ids of group next + 1
+      Page next = fetch(0, id2);
+      if (groups > 1) id2 = fetch_id(1);
+      Page cur = next;
+      float lv = 0.f, top = 0.f;
+      int e_ref = 0;       // E
+      int32_t v_id = 0;    // the page of the V tile that is next
+      for (int t = 0; ok && t <= sp.tiles; ++t) {
         if (t < sp.tiles) {
-          cur = nxt;
-          nxt = nn;
-          sc = nsc;
-          if (mine && t + 2 < sp.tiles) nn = fetch(t + 2);
-          if (mine && t + 1 < sp.tiles) nsc = fetch_scales(t + 1, nxt);
-          if (!acquire()) {
+          const int in = t % kGroup;
+          if (in == 0) {
+            cur = next;
+            const int group = t / kGroup;
+            if (group + 1 < groups) next = fetch(group + 1, id2);
+            if (group + 2 < groups) id2 = fetch_id(group + 2);
+            lv = fminf(fmaxf(log2f(cur.vs), -100.f), 100.f);
+            top = lv;  // the largest of each tile's pages
+#pragma unroll
+            for (int m = 1; m < kNB; m <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+          }
+          const int from = in * kNB + (lane < kNB ? lane : 0);
+          const int32_t id = __shfl_sync(0xffffffffu, cur.id, from);
+          const float ks = __shfl_sync(0xffffffffu, cur.ks, from);
+          const float my_lv = __shfl_sync(0xffffffffu, lv, from);
+          const int e_top = static_cast<int>(
+              floorf(__shfl_sync(0xffffffffu, top, in * kNB)));
+          if (t == 0 || e_top > e_ref + kVsSlack) e_ref = e_top;
+          // A slot is written again kScaleSlots tiles on.  K tile t is copied
+          // at most kRaw tiles ahead of the one being converted, which is at
+          // most kStages ahead of the one whose S is next, at most two ahead
+          // of the one in the softmax: kRaw + kStages + 2 < kScaleSlots, so
+          // the slot's old readers are past it once the copy may start.
+          if (g + t >= kRaw &&
+              !warp_wait(raw_empty0 + 8 * ((g + t) % kRaw),
+                         (((g + t) / kRaw) - 1) & 1)) {
             ok = false;
             break;
-          }
-          // A slot is written again kScaleSlots tiles on.  K tile t is copied
-          // at most two tiles ahead of the one being converted, which is at
-          // most kStages ahead of the one whose S is next, at most two ahead
-          // of the one in the softmax: the slot's old readers are past it.
-          const float lv =
-              mine ? fminf(fmaxf(log2f(sc.y), -100.f), 100.f) : -100.f;
-          float top = lv;
-#pragma unroll
-          for (int m = 1; m < kNB; m <<= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-          const int e_top =
-              static_cast<int>(floorf(__shfl_sync(0xffffffffu, top, 0)));
-          int grow = 0;
-          if (t == 0) {
-            e_ref = e_top;
-          } else if (e_top > e_ref + kVsSlack) {
-            grow = max(e_ref - e_top, -126);
-            e_ref = e_top;
           }
           float* to = scale_s + ((g + t) % kScaleSlots) * kSlotFloats;
-          if (mine) {
+          if (lane < kNB) {
             const float lvn =
-                fmaxf(lv - static_cast<float>(e_ref), -96.f) + kShift;
-            to[p] = sc.x;
-            to[kNB + p] = lvn;
-            to[2 * kNB + p] = exp2f(-lvn);
+                fmaxf(my_lv - static_cast<float>(e_ref), -96.f) + kShift;
+            to[lane] = ks;
+            to[kNB + lane] = lvn;
+            to[2 * kNB + lane] = exp2f(-lvn);
           }
-          if (lane == 0) {
-            to[kSlotFloats - 2] = dev::exp2_int(grow);
-            to[kSlotFloats - 1] = static_cast<float>(e_ref);
-          }
-          copy(a.k_cache, kvh, cur);
+          if (lane == 0) to[kSlotFloats - 1] = static_cast<float>(e_ref);
+          __syncwarp();  // before lane 0's arrival publishes them
+          ok = copy(0, g + t, a.k_cache, kvh, id);
+          if (ok && t >= 1) ok = copy(1, g + t - 1, a.v_cache, kvh, v_id);
+          v_id = id;
+        } else {
+          ok = copy(1, g + t - 1, a.v_cache, kvh, v_id);
         }
-        if (t >= 1) {
-          if (!acquire()) {
-            ok = false;
-            break;
-          }
-          copy(a.v_cache, kvh, prv);
-        }
-        prv = cur;
       }
       if (bad_id) dev::set_error(a.dev_err, PA_ERR_DEVICE_OOB);
       g += sp.tiles;
@@ -494,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd = dev::sw128_desc(base + Lay::kOffV, kTileHalf, 1024);
       uint32_t g = 0;   // K/V tiles of this CTA's earlier items
       uint32_t ts = 0;  // S tiles issued (query tile x)
+      uint32_t ps = 0;  // and P.V
       int v = 0;        // items
       // S(t) = Q K(t)^T: the dims whose q is in tensor memory need no read of
       // the A operand from shared memory, which at 64 keys a tile is what
@@ -555,23 +575,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt =
             __shfl_sync(0xffffffffu, x ? sp.n_tiles[1] : sp.n_tiles[0], 0);
         const int tiles = __shfl_sync(0xffffffffu, sp.tiles, 0);
+        const int stride = __shfl_sync(0xffffffffu, sp.stride, 0);
+        const int first = stride == 2 ? x : 0;
+        int kt = 0, vt = 0;  // K and V tiles of the item released so far
+        // S of this query tile's j-th key tile, past the tiles between.
+        auto s_of = [&](int j) -> bool {
+          for (const int t = first + j * stride; kt < t; ++kt)
+            if (!skip(g + kt, k_full0, k_empty0)) return false;
+          return issue_s(g + kt++, j + 1 == nt);
+        };
+        auto pv_of = [&](int j) -> bool {
+          for (const int t = first + j * stride; vt < t; ++vt)
+            if (!skip(g + vt, v_full0, v_empty0)) return false;
+          return issue_pv(g + vt++, ps++, j == 0);
+        };
         if (nt > 0) {
-          ok = warp_wait(q_full0 + 8 * x, v & 1) && issue_s(g, nt == 1);
+          ok = warp_wait(q_full0 + 8 * x, v & 1) && s_of(0);
           ++v;
-        } else {
-          ok = skip(g, k_full0, k_empty0);
         }
         // S(j+1) goes ahead of P(j).V, which waits for the softmax.
-        for (int j = 0; ok && j < tiles; ++j) {
-          if (j + 1 < nt)
-            ok = issue_s(g + j + 1, j + 2 == nt);
-          else if (j + 1 < tiles)
-            ok = skip(g + j + 1, k_full0, k_empty0);
-          if (!ok) break;
-          if (j < nt)
-            ok = issue_pv(g + j, ts - (j + 1 < nt ? 2 : 1), j == 0);
+        for (int j = 0; ok && j < nt; ++j)
+          ok = (j + 1 >= nt || s_of(j + 1)) && pv_of(j);
+        // Tiles past its last one, K a tile ahead of V as they are converted.
+        while (ok && vt < tiles) {
+          if (kt < tiles && kt <= vt + 1)
+            ok = skip(g + kt++, k_full0, k_empty0);
           else
-            ok = skip(g + j, v_full0, v_empty0);
+            ok = skip(g + vt++, v_full0, v_empty0);
         }
         g += tiles;
       }
@@ -601,21 +631,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int e0 = row0 * 128 + (((2 * cc) ^ (row0 & 7)) << 4);
     const int e1 = row0 * 128 + (((2 * cc + 1) ^ (row0 & 7)) << 4);
     constexpr int kPer = kKeys / 32 * kHalves;  // chunks per thread and tile
-    uint32_t u = 0, g = 0;
+    uint32_t g = 0;
     bool ok = true;
-    // Raw tile u into the fp16 tile at offset `dst`, the n-th to be put there,
-    // once `empty` says that the one before was read; rows from `limit` on
-    // become zeros (a key past the context has weight 0, but 0 * NaN is NaN
-    // in the MMA).
-    auto convert = [&](int dst, uint32_t full, uint32_t empty, uint32_t n,
-                       int limit) -> bool {
-      const uint32_t slot = u % kRaw;
-      if (!warp_wait(raw_full0 + 8 * slot, (u / kRaw) & 1) ||
-          (n >= 1 && !warp_wait(empty, (n - 1) & 1)))
+    // Tile t of K (w = 0) or V (w = 1) into its stage, once the one before
+    // there was read; rows from `limit` on become zeros (a key past the context
+    // has weight 0, but 0 * NaN is NaN in the MMA).
+    auto convert = [&](int w, uint32_t t, int limit) -> bool {
+      const uint32_t slot = w * kRaw + t % kRaw, s = t % kStages;
+      if (!warp_wait(raw_full0 + 8 * slot, (t / kRaw) & 1) ||
+          (t >= kStages && !warp_wait((w ? v_empty0 : k_empty0) + 8 * s,
+                                      ((t / kStages) - 1) & 1)))
         return false;
       const uint8_t* raw = smem + Lay::kOffRaw + slot * Lay::kRawTile +
                            row0 * D + cc * 16;
-      uint8_t* d = smem + dst;
+      uint8_t* d = smem + (w ? Lay::kOffV : Lay::kOffK) + s * Lay::kTile;
       auto chunk = [&](int row_step, int half, bool zero) {
         uint4 w = *reinterpret_cast<const uint4*>(raw + row_step * D +
                                                   half * 64);
@@ -640,9 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       dev::fence_proxy_async_smem();  // visible to the tensor cores
       __syncwarp();
-      warp_arrive(full);
+      warp_arrive((w ? v_full0 : k_full0) + 8 * s);
       warp_arrive(raw_empty0 + 8 * slot);
-      ++u;
       return true;
     };
     for (int n = 0; ok; ++n) {
@@ -652,17 +680,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.state == kSkip) continue;
       const Span sp = span_of(it);
       for (int t = 0; ok && t <= sp.tiles; ++t) {
-        if (t < sp.tiles) {
-          const uint32_t s = (g + t) % kStages;
-          ok = convert(Lay::kOffK + s * Lay::kTile, k_full0 + 8 * s,
-                       k_empty0 + 8 * s, (g + t) / kStages, kKeys);
-        }
-        if (ok && t >= 1) {
-          const uint32_t s = (g + t - 1) % kStages;
-          ok = convert(Lay::kOffV + s * Lay::kTile, v_full0 + 8 * s,
-                       v_empty0 + 8 * s, (g + t - 1) / kStages,
-                       it.L - (t - 1) * kKeys);
-        }
+        if (t < sp.tiles) ok = convert(0, g + t, kKeys);
+        if (ok && t >= 1)
+          ok = convert(1, g + t - 1, it.L - (t - 1) * kKeys);
       }
       g += sp.tiles;
     }
@@ -689,6 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t g = 0;   // K/V tiles of this CTA's earlier items (scale slots)
   uint32_t ts = 0;  // S tiles of this query tile so far
   int v = 0;        // items so far
+  int halves = 0;   // of which the pair shared the keys
+  float* merge = reinterpret_cast<float*>(smem + Lay::kOffMerge) + r;
   for (int n = 0; ok; ++n) {
     Item it;
     ok = next_item(n, it);
@@ -780,7 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(q_full);
       ++v;
     }
-    float m_ref = -INFINITY, l = 0.f;
+    float m_ref = 0.f, l = 0.f, e_ref = 0.f;  // e_ref: E
+    const int first = sp.stride == 2 ? x : 0;
     for (int j = 0; j < n_tiles && ok; ++j, ++ts) {
       ok = warp_wait(s_full, ts & 1);
       if (!ok) break;
@@ -805,7 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(p_full);
         continue;
       }
-      const int lim = qpos - j * kKeys;  // the last key this row sees
+      const int tile = first + j * sp.stride;
+      const int lim = qpos - tile * kKeys;  // the last key this row sees
       if (lim < kKeys - 1) {
 #pragma unroll
         for (int k = 0; k < kKeys; ++k)
@@ -813,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The row's maximum, by blocks: a factor c_row ks_b for each (never 0:
       // -inf * 0 is NaN).
-      const float* sc = scale_s + ((g + j) % kScaleSlots) * kSlotFloats;
+      const float* sc = scale_s + ((g + tile) % kScaleSlots) * kSlotFloats;
       float cb[kNB];
       float mx = -INFINITY;
 #pragma unroll
@@ -838,15 +862,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) *
                            cb[b]);
       }
-      float factor = sc[kSlotFloats - 2];  // 1, or what E grew by
+      // O's factor for what E grew by since this row's last tile (1: not)
+      const float e_now = sc[kSlotFloats - 1];
+      float factor = 1.f;
       if (j == 0) {
-        m_ref = mx;  // O is still empty: the first P.V overwrites it
-      } else if (mx > m_ref + kRescaleLog2) {
-        const float f = dev::fast_exp2(m_ref - mx);
-        m_ref = mx;
-        l *= f;
-        factor *= f;
+        // O is still empty: the first P.V overwrites it.  (A row may see no
+        // key of tile 1's first tile: finite, so that its weights are 0.)
+        m_ref = fmaxf(mx, -1e30f);
+      } else {
+        factor = dev::fast_exp2(e_ref - e_now);
+        if (mx > m_ref + kRescaleLog2) {
+          const float f = dev::fast_exp2(m_ref - mx);
+          m_ref = mx;
+          l *= f;
+          factor *= f;
+        }
       }
+      e_ref = e_now;
       if (__any_sync(0xffffffffu, factor != 1.f)) {
         // Rare (the maxima settle): a rolled loop over 16 columns, which
         // leaves the scores in their registers.
@@ -902,39 +934,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The item's output: O 2^(E - shift) / l -> out[token, query head].
     // (The phase before it was waited for with the last tile's P.)
     if (ok) ok = warp_wait(o_done, (ts - 1) & 1);
-    if (ok && !idle) {
+    // Factors of O and, where the pair shared the keys, of tile 1's O.
+    float f0 = dev::exp2_int(static_cast<int>(e_ref - kShift)), f1 = 0.f;
+    if (ok && sp.stride == 2) {
+      if (x == 1) {
+        merge[0] = m_ref;
+        merge[kRows] = l;
+        merge[2 * kRows] = e_ref;
+        dev::tc_fence_before();
+        __syncwarp();
+        warp_arrive(half_done);
+        // the next item's P.V may overwrite O once tile 0 has read it
+        ok = warp_wait(half_read, halves & 1);
+      } else {
+        ok = warp_wait(half_done, halves & 1);
+        if (ok) {
+          const float m1 = merge[0], l1 = merge[kRows];
+          const float top = fmaxf(m_ref, m1);
+          const float w0 = dev::fast_exp2(m_ref - top);
+          const float w1 = dev::fast_exp2(m1 - top);
+          l = l * w0 + l1 * w1;
+          f0 *= w0;
+          f1 = w1 *
+               dev::exp2_int(static_cast<int>(merge[2 * kRows] - kShift));
+        }
+      }
+      ++halves;
+    }
+    if (ok && !idle && (x == 0 || sp.stride == 1)) {
       dev::tc_fence_after();
       // l is above 0 (each row sees a key) or NaN, which is passed on
-      const float e_last = scale_s[((g + n_tiles - 1) % kScaleSlots) *
-                                       kSlotFloats + kSlotFloats - 1];
-      const float inv =
-          dev::exp2_int(static_cast<int>(e_last - kShift)) / l;
+      const float inv = 1.f / l;
+      f0 *= inv;
+      f1 *= inv;
       T* dst = static_cast<T*>(a.out) + row_at;
       float* dst32 = static_cast<float*>(a.out) + row_at;  // out_f32 only
-#pragma unroll
+#pragma unroll 1
       for (int col = 0; col < D; col += 32) {
         float ov[32];
         dev::tmem_ld32(o_tmem + col, ov);
         dev::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] *= f0;
+        if (sp.stride == 2) {
+          float o1[32];
+          dev::tmem_ld32(o_tmem + 128 + col, o1);
+          dev::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = fmaf(o1[e], f1, ov[e]);
+        }
         if (valid && a.out_f32) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(dst32 + col + e) =
-                make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv,
-                            ov[e + 3] * inv);
+                make_float4(ov[e], ov[e + 1], ov[e + 2],
+                            ov[e + 3]);
         } else if (valid) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint4 w;
-            w.x = dev::Mma<T>::pack(ov[e] * inv, ov[e + 1] * inv);
-            w.y = dev::Mma<T>::pack(ov[e + 2] * inv, ov[e + 3] * inv);
-            w.z = dev::Mma<T>::pack(ov[e + 4] * inv, ov[e + 5] * inv);
-            w.w = dev::Mma<T>::pack(ov[e + 6] * inv, ov[e + 7] * inv);
+            w.x = dev::Mma<T>::pack(ov[e], ov[e + 1]);
+            w.y = dev::Mma<T>::pack(ov[e + 2], ov[e + 3]);
+            w.z = dev::Mma<T>::pack(ov[e + 4], ov[e + 5]);
+            w.w = dev::Mma<T>::pack(ov[e + 6], ov[e + 7]);
             *reinterpret_cast<uint4*>(dst + col + e) = w;
           }
         }
       }
       dev::tc_fence_before();
+    }
+    if (ok && sp.stride == 2 && x == 0) {
+      __syncwarp();
+      warp_arrive(half_read);
     }
     g += sp.tiles;
   }
@@ -947,9 +1018,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 
-template <typename T, int BS, int G, int D>
+template <typename T, int BS, int G, int D, bool kShareKeys>
 pa_status launch(const PrefillQ8Args& a, cudaStream_t st) {
-  auto kern = prefill_q8_kernel<T, BS, G, D>;
+  auto kern = prefill_q8_kernel<T, BS, G, D, kShareKeys>;
   const size_t smem = LayoutQ8<D>::kSmemBytes;
   static OncePerDevice configured;
   cudaError_t e = cudaSuccess;
@@ -990,14 +1061,25 @@ pa_status launch(const PrefillQ8Args& a, cudaStream_t st) {
   return PA_OK;
 }
 
+// A call whose sequences have at most one query tile of new tokens runs with
+// kShareKeys: 218 draft rows over 72k cached tokens 89 us instead of 110.  As
+// a branch of the one kernel it cost the others 3 to 5 % (registers).
+template <typename T, int BS, int G, int D>
+pa_status dispatch_share(const pa_prefill_desc* d, const PrefillQ8Args& a,
+                         cudaStream_t st) {
+  return static_cast<int64_t>(d->max_q_len) * G <= kRows
+             ? launch<T, BS, G, D, true>(a, st)
+             : launch<T, BS, G, D, false>(a, st);
+}
+
 template <typename T, int BS, int D>
 pa_status dispatch_group(const pa_prefill_desc* d, const PrefillQ8Args& a,
                          cudaStream_t st) {
   switch (d->num_q_heads / d->num_kv_heads) {
-    case 1: return launch<T, BS, 1, D>(a, st);
-    case 2: return launch<T, BS, 2, D>(a, st);
-    case 4: return launch<T, BS, 4, D>(a, st);
-    default: return launch<T, BS, 8, D>(a, st);
+    case 1: return dispatch_share<T, BS, 1, D>(d, a, st);
+    case 2: return dispatch_share<T, BS, 2, D>(d, a, st);
+    case 4: return dispatch_share<T, BS, 4, D>(d, a, st);
+    default: return dispatch_share<T, BS, 8, D>(d, a, st);
   }
 }
 
