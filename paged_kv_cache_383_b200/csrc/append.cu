@@ -272,6 +272,9 @@ __device__ __forceinline__ void token_rows(const AppendArgs& a, int t0,
   if (a.query_start) {
     __syncthreads();
     for (int j = tid; j < a.num_seqs; j += kThreads) {
+      // The first CTA checks every sequence: one whose range holds no row is
+      // met by no token.
+      if (!kQ8 && blockIdx.x == 0) read_seq(a, j);
       const int lo = max(a.query_start[j], t0);
       const int hi = min(a.query_start[j + 1], t0 + n_tok);
       for (int t = lo; t < hi; ++t) s_seq[t - t0] = j;
@@ -510,7 +513,12 @@ __device__ __forceinline__ void window_kv(const AppendArgs& a, int w,
   } else {
     for (int j = tid; j < a.num_seqs; j += kThreads) {
       const int q0 = a.query_start[j], q1 = a.query_start[j + 1];
-      if (q1 <= lo || q0 >= hi) continue;
+      if (q1 <= lo || q0 >= hi) {
+        // The first CTA checks every sequence: one whose range holds no row
+        // is met by no window.
+        if (blockIdx.x == 0) read_seq(a, j);
+        continue;
+      }
       const Seq sq = read_seq(a, j);
       if (!sq.ok) continue;
       const int from = max(q0, lo);
@@ -673,6 +681,11 @@ pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
   if (d->rot_dim > 0 && !rope_freqs)
     return fail(PA_ERR_INVALID_ARG, "%s: rot_dim %d without rope_freqs", fn,
                 d->rot_dim);
+  if (q && q_out == q && d->total_q > 1 && d->q_stride != d->q_out_stride)
+    return fail(PA_ERR_INVALID_ARG,
+                "%s: q_out is q, but their strides %lld and %lld differ", fn,
+                static_cast<long long>(d->q_out_stride),
+                static_cast<long long>(d->q_stride));
   const void* aligned[8] = {q_out, k_cache, v_cache, q, k, v, q_norm, k_norm};
   for (const void* p : aligned)
     if (!aligned16(p))
@@ -740,7 +753,8 @@ pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
     while (query_start && a.window < kMaxWindow &&
            units / a.window > 8LL * device_sm_count())
       a.window *= 2;
-    const int64_t windows = (d->total_q + a.window - 1) / a.window;
+    const int64_t windows =
+        (static_cast<int64_t>(d->total_q) + a.window - 1) / a.window;
     if (windows * a.unit_groups + ctas > 0x7fffffffLL)
       return fail(PA_ERR_UNSUPPORTED, "%s: %d rows are too many", fn,
                   d->total_q);

@@ -72,6 +72,14 @@ def test_append_rejects_null_and_misaligned(pkv, name):
 
 
 @pytest.mark.parametrize("name", ["pa_append", "pa_append_q8"])
+def test_append_in_place_needs_one_stride(pkv, name):
+    """q_out == q (here all pointers are) with another row stride."""
+    from paged_kv_cache_383_b200 import _lib
+    assert _call(name, _append_desc(q_out_stride=1536)) == 1
+    assert b"strides" in _lib.load().pa_last_error()
+
+
+@pytest.mark.parametrize("name", ["pa_append", "pa_append_q8"])
 def test_append_of_nothing_is_a_noop(pkv, name):
     n = 12 if name == "pa_append" else 14
     for kw in (dict(num_seqs=0, total_q=0), dict(total_q=0),

@@ -411,6 +411,74 @@ def test_device_errors(pkv, q8):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+def test_device_errors_without_rows(pkv, q8):
+    """A sequence whose range holds no row of the call, but is no valid empty
+    one, sets dev_err all the same; padding (length 0) never does."""
+    from paged_kv_cache_383_b200 import _lib
+
+    def run(lens_at, start, flagged):
+        x = Batch(torch.float16, 4, 2, 64, 16, [20, 33, 8], [3, 5, 8],
+                  norm=False, rot=64, layout="half", spare_rows=0)
+        pool = random_q8(x) if q8 else [
+            torch.zeros(x.shape, device="cuda", dtype=x.dtype) for _ in "kv"]
+        table, lens, _ = x.args()
+        for i, n in lens_at.items():
+            lens[i] = n
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q_out = torch.zeros_like(x.q)
+        (pkv.pa_append_q8 if q8 else pkv.pa_append)(
+            q_out, *pool, x.q, x.k, x.v, table, lens,
+            torch.tensor(start, dtype=torch.int32, device="cuda"),
+            dev_err=err, **x.kw)
+        torch.cuda.synchronize()
+        assert err.item() == (_lib.PA_ERR_DEVICE_OOB if flagged else 0)
+        assert q_out[:3].abs().sum() > 0
+
+    run({}, [0, 3, 3, 3], False)
+    run({}, [0, 3, 2, 2], True)             # ends before it starts
+    run({}, [0, 3, 16, 20], True)           # past the rows
+    run({1: -4}, [0, 3, 3, 3], True)        # no rows, a bad length
+    run({2: 49}, [0, 3, 3, 3], True)        # the table has 48 tokens
+    run({1: 0, 2: 0}, [0, 3, 3, 40], False)  # padding
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_queries_in_place(pkv, q8):
+    """q_out is q itself, a slice of the projection."""
+    x = Batch(torch.bfloat16, 8, 2, 128, 16, [40, 0, 17], [5, 2, 17],
+              norm=True, rot=128, layout="interleaved")
+    fn = pkv.pa_append_q8 if q8 else pkv.pa_append
+    outs = []
+    for in_place in (False, True):
+        pool = random_q8(x) if q8 else [
+            torch.zeros(x.shape, device="cuda", dtype=x.dtype) for _ in "kv"]
+        q_out = x.q if in_place else x.q.clone()
+        fn(q_out, *pool, x.q, x.k, x.v, *x.args(), **x.kw)
+        torch.cuda.synchronize()
+        outs.append([q_out.contiguous()] + [p.clone() for p in pool])
+    for a, b in zip(*outs):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_keys_and_values_only(pkv, q8):
+    """No query heads: the cache gets what a call with them writes."""
+    x = Batch(torch.float16, 4, 3, 64, 32, [70, 33], [40, 33], norm=True,
+              rot=32, layout="half")
+    fn = pkv.pa_append_q8 if q8 else pkv.pa_append
+    pools = []
+    for with_q in (True, False):
+        pool = random_q8(x) if q8 else [
+            torch.zeros(x.shape, device="cuda", dtype=x.dtype) for _ in "kv"]
+        q, q_out = (x.q, torch.empty_like(x.q)) if with_q else (None, None)
+        fn(q_out, *pool, q, x.k, x.v, *x.args(), **x.kw)
+        torch.cuda.synchronize()
+        pools.append(pool)
+    for a, b in zip(*pools):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("q8", [False, True])
 def test_graph_and_stream(pkv, q8):
     """Captured and replayed with other lengths and values, on a stream of
     its own, equals eager calls."""
