@@ -411,8 +411,8 @@ pa_status pa_swap_blocks(void* dst_k_cache, void* dst_v_cache,
  * [rot_dim / 2], e.g. from pa_rope_freqs.  The caches as for pa_decode.
  * Supported: head_dim 64 or 128, block_size 16 or 32, rot_dim a multiple of
  * 16 up to head_dim.
- * A sequence with context length 0 is padding: its rows are neither read nor
- * written.  Rows behind the last sequence, and every cache slot but the new
+ * A sequence with context length 0 is padding: nothing is written for its
+ * rows, whatever they hold.  Rows behind the last sequence, and every cache slot but the new
  * tokens', stay as they are.
  * Two sequences must not append to one physical block in one call (copy
  * shared blocks first).  Device-side: a context or query range outside the
@@ -522,7 +522,11 @@ pa_status pa_append_q8(void* q_out, void* k_cache, void* v_cache,
  * and out; kernel PA_KERNEL_SIMT is PA_ERR_UNSUPPORTED), workspace
  * (pa_decode_workspace_bytes), launches, checks and errors.  Products of q
  * and the weights with the codes run on the tensor cores in fp16 (the codes
- * are exact there), scales and softmax in fp32. */
+ * are exact there), scales and softmax in fp32.  A weight times its block's
+ * v scale is kept in fp16 relative to the largest v scale of the context: to
+ * 2^-11 of itself, but to no less than about 2^-33 of that largest scale
+ * (prefill alike), so a block whose scale is below 2^-20 of it is less
+ * precise the smaller it is. */
 pa_status pa_decode_q8(void* out, const void* q, const void* k_cache,
                        const void* v_cache, const float* k_scales,
                        const float* v_scales, const int32_t* block_tables,

@@ -31,13 +31,21 @@
 //    output's own rounding is and an eighth of a bf16 output's, so no
 //    residual is added.
 //
-// Work items, the persistent grid (two CTAs per SM), the query tiles of 128
+// The longest-first work items, the persistent grid, the query tiles of 128
 // rows and the barriers' discipline (each counted over the CTA's tiles,
-// waited on in order, never two phases ahead) are pa_prefill's
-// (prefill.cu).  Warps: 0..3 hold one query row per thread: they load and
-// convert its q, and run the softmax; 4..7 convert K and V; 8 takes the
-// items, copies pages (contiguous in this layout: one bulk copy each) and
-// stages their scales; 9 issues the MMAs.
+// waited on in order, never two phases ahead) are pa_prefill's (prefill.cu).
+// Here one CTA has an SM to itself and an item is a pair of query tiles, which
+// share the converted keys and take turns on the tensor cores.  Warps 0..3 and
+// 4..7, one query row per thread, load and convert q and run the softmax of
+// one tile each; 8..11 convert K and V; 12 takes the items, copies pages
+// (contiguous in this layout: one bulk copy each) and stages their scales; 13
+// and 14 issue the MMAs, whole warps with an elected thread (a lone thread
+// spends about 90 cycles on each).  Half of q's dims sit in tensor memory: at
+// 64 keys a tile, reading both operands of S from shared memory bounds it.
+// 8 chunks of 512 rows over 26k tokens with 64 query heads: 634 us, against
+// 767 with one query tile per CTA and two CTAs per SM, 721 with 128-key tiles.
+// A tile pair takes about 2600 cycles of an SM; its MMAs need 1450 and its
+// exponentials 1024, the rest is the latency between the steps.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -108,9 +116,9 @@ struct PrefillQ8Args {
   int num_items;
 };
 
-// raw_full[], raw_empty[] (of K, then of V), k_full[], k_empty[], v_full[], v_empty[]; for each
-// of the pair q_full, q_empty, s_full, s_free, p_full, o_done; done; item_full[2],
-// item_empty[2].
+// raw_full[], raw_empty[] (of K, then of V), k_full[], k_empty[], v_full[],
+// v_empty[]; for each of the pair q_full, q_empty, s_full, s_free, p_full,
+// o_done; half_done, half_read; done; item_full[2], item_empty[2].
 constexpr int kNumBars = 4 * kRaw + 4 * kStages + 6 * kPair + 2 + 1 + 4;
 constexpr int kItemWords = 8;
 
@@ -454,9 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t == 0 || e_top > e_ref + kVsSlack) e_ref = e_top;
           // A slot is written again kScaleSlots tiles on.  K tile t is copied
           // at most kRaw tiles ahead of the one being converted, which is at
-          // most kStages ahead of the one whose S is next, at most two ahead
-          // of the one in the softmax: kRaw + kStages + 2 < kScaleSlots, so
-          // the slot's old readers are past it once the copy may start.
+          // most kStages ahead of the one whose S is next, at most two of a
+          // query tile's own ahead of the one in its softmax (four where the
+          // pair shares the keys): kRaw + kStages + 4 < kScaleSlots, so the
+          // slot's old readers are past it once the copy may start.
           if (g + t >= kRaw &&
               !warp_wait(raw_empty0 + 8 * ((g + t) % kRaw),
                          (((g + t) / kRaw) - 1) & 1)) {
@@ -868,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j == 0) {
         // O is still empty: the first P.V overwrites it.  (A row may see no
         // key of tile 1's first tile: finite, so that its weights are 0.)
-        m_ref = fmaxf(mx, -1e30f);
+        m_ref = fmaxf(mx, -3e38f);
       } else {
         factor = dev::fast_exp2(e_ref - e_now);
         if (mx > m_ref + kRescaleLog2) {

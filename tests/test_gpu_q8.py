@@ -409,6 +409,51 @@ def test_prefill(pkv, case, pow2):
     assert (out[n:] == 0).all()
 
 
+@pytest.mark.parametrize("hq,hkv,new", [(16, 2, 16), (8, 1, 17), (4, 4, 128),
+                                        (4, 4, 129), (8, 4, 3)])
+def test_prefill_few_new_tokens(pkv, hq, hkv, new):
+    """Up to 128 rows per KV head, where a sequence's keys are split between
+    the query tiles, and just past it: contexts of one key tile, of two, of
+    odd and even counts, ends inside and at the edge of a tile."""
+    ctx = [new, new + 1, 64, 65, 127, 128, 129, 191, 193, 256, 640, 641]
+    ctx = [max(c, new) for c in ctx] + [1]
+    n = [new] * (len(ctx) - 1) + [1]
+    n[5], n[8] = 1, min(2, new)
+    pool = Pool(hkv, 128, 16, ctx, seed=hq + new)
+    start = np.concatenate([[0], np.cumsum(n)])
+    q = torch.randn(int(start[-1]), hq, 128, device="cuda").to(HF)
+    out32, out = prefill(pkv, pool, q, start, 0.09, new)
+    pos = positions(ctx, n)
+    ref, mag = reference(pool, q, pos, 0.09)
+    check_prefill(out32, out, ref, bound_prefill(pool, q, pos, 0.09, mag),
+                  len(q))
+
+
+def test_two_calls_at_once(pkv):
+    """Two streams, each call with its own workspace, give what one call
+    after the other gives."""
+    pools = [Pool(4, 128, 16, [900, 33, 300], seed=s) for s in (50, 51)]
+    qs = [torch.randn(60, 16, 128, device="cuda").to(BF) for _ in "12"]
+    start = torch.tensor([0, 40, 53, 60], dtype=torch.int32, device="cuda")
+    streams = [torch.cuda.Stream() for _ in "12"]
+
+    def both(streams):
+        outs = []
+        for pool, q, s in zip(pools, qs, streams):
+            a, b = torch.empty_like(q), torch.empty_like(q[:3])
+            pkv.pa_prefill_q8(a, q, *pool.cache, *pool.dev, start, 0.09,
+                              max_q_len=40, stream=s)
+            pkv.pa_decode_q8(b, q[:3], *pool.cache, *pool.dev, 0.09, stream=s)
+            outs += [a, b]
+        torch.cuda.synchronize()
+        return outs
+    torch.cuda.synchronize()
+    one = both([None, None])
+    for _ in range(5):
+        for x, y in zip(one, both(streams)):
+            assert torch.equal(x, y)
+
+
 def test_prefill_many_items(pkv):
     """More work items than CTAs, of very unlike lengths."""
     rng = np.random.default_rng(5)
