@@ -656,6 +656,11 @@ def pa_decode_q8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
         desc = make_desc(q, k_cache, block_tables,
                          partition_size=partition_size,
                          max_context_len=max_context_len, reduce=reduce)
+    elif ((desc.num_seqs, desc.num_q_heads, desc.head_dim) != q.shape or
+          (desc.num_seqs, desc.max_blocks_per_seq) != block_tables.shape or
+          (desc.num_blocks, desc.num_kv_heads, desc.block_size,
+           desc.head_dim) != k_cache.shape or desc.dtype != _code(q.dtype)):
+        raise ValueError("desc does not describe q, k_cache and block_tables")
     _out_mode(desc, out, q.dtype)
     if workspace is None:
         workspace = _workspace(

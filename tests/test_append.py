@@ -255,6 +255,25 @@ def test_python_refusals(pkv):
         pkv.pa_append_q8(None, kc, kc, s[:3], s, None, row, row, t, n)
 
 
+def test_decode_q8_refuses_a_stale_descriptor(pkv):
+    """A descriptor made for other shapes would send the kernel past the
+    tensors' ends."""
+    import torch
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(5, 2, 16, 64).to(torch.float8_e4m3fn)
+    ks = torch.ones(5, 2)
+    table = torch.zeros(2, 3, dtype=torch.int32)
+    lens = torch.zeros(2, dtype=torch.int32)
+    for dq, dkc, dt in ((q.repeat(2, 1, 1), kc, table.repeat(2, 1)),
+                        (q.repeat(1, 2, 1), kc, table),
+                        (q, kc.repeat(2, 1, 1, 1), table),
+                        (q, kc, table.repeat(1, 2)), (q.half(), kc, table)):
+        desc = pkv.make_desc(dq, dkc, dt)
+        with pytest.raises(ValueError, match="desc does not describe"):
+            pkv.pa_decode_q8(torch.empty_like(q), q, kc, kc, ks, ks, table,
+                             lens, 0.1, desc=desc)
+
+
 def test_oracle_e4m3():
     import torch
     codes = np.arange(256, dtype=np.uint8)
