@@ -199,7 +199,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
 }
 
 // kShareKeys: for calls whose items all have at most 128 rows (host rule in
-// launch): the pair of query tiles shares an item's keys (see Span).
+// dispatch_share): the pair of query tiles shares an item's keys (see Span).
 template <typename T, int BS, int G, int D, bool kShareKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q8_kernel(const PrefillQ8Args a) {
@@ -1070,13 +1070,17 @@ pa_status launch(const PrefillQ8Args& a, cudaStream_t st) {
   return PA_OK;
 }
 
-// A call whose sequences have at most one query tile of new tokens runs with
-// kShareKeys: 218 draft rows over 72k cached tokens 89 us instead of 110.  As
-// a branch of the one kernel it cost the others 3 to 5 % (registers).
+// A call whose sequences have at most one query tile of new tokens, and
+// contexts that may exceed four key tiles, runs with kShareKeys.  4 new tokens
+// of 256 sequences, 64 query heads: contexts of 1500 tokens 377 us instead of
+// 442, of 300 137 instead of 145, but of 128 100 instead of 96 and of 64 88
+// instead of 81; 218 draft rows over 72k cached tokens 89 instead of 110.  As a
+// branch of the one kernel it cost the others 3 to 5 % (registers).
 template <typename T, int BS, int G, int D>
 pa_status dispatch_share(const pa_prefill_desc* d, const PrefillQ8Args& a,
                          cudaStream_t st) {
-  return static_cast<int64_t>(d->max_q_len) * G <= kRows
+  return static_cast<int64_t>(d->max_q_len) * G <= kRows &&
+                 a.max_context_len > 4 * kKeys
              ? launch<T, BS, G, D, true>(a, st)
              : launch<T, BS, G, D, false>(a, st);
 }
