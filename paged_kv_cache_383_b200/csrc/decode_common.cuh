@@ -231,13 +231,17 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
   const int lane = threadIdx.x & 31;
   dev::pdl_trigger();
   const int ctx = a.context_lens[b];
+  // The decode kernel has completed and its partials are visible.  CTAs with
+  // nothing to do wait too: were they to leave at once, this grid could be
+  // over before the decode is, and the kernel launched behind it, which waits
+  // for this grid only, would overwrite what the decode still reads.
+  dev::pdl_wait();
   if (ctx < 0 || ctx > a.max_blocks_per_seq * block_size ||
       ctx > a.max_context_len)
     return;  // flagged by the decode kernel
   const int n_parts = ctx > 0 ? (ctx + a.partition_size - 1) / a.partition_size
                               : 1;
   if (n_parts <= 1) return;  // the decode kernel wrote this row itself
-  dev::pdl_wait();           // partials of the decode kernel are visible
 
   const int64_t row0 =
       (static_cast<int64_t>(b) * a.num_q_heads + qh) * a.max_parts;

@@ -1,0 +1,73 @@
+"""Calls queued one behind the other on a stream give what the same calls give
+with a synchronisation after each."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_decode_then_append_of_the_next_step(pkv, q8):
+    """A table so wide that the decode may have 32 partitions (its separate
+    reduce runs) and contexts of one partition each (which leave the reduce
+    nothing to do); the append behind it overwrites the queries that the
+    decode reads, moves the scales of the blocks it reads and writes into
+    them."""
+    hq, hkv, d, bs, n, steps = 64, 8, 128, 16, 4, 8
+    width = 131072 // bs
+    g = torch.Generator(device="cuda").manual_seed(1)
+    # the last block of each context holds 3 tokens before the first step
+    first = [4000 - 13 - 64 * b for b in range(n)]
+    used = [-(-(c + steps) // bs) for c in first]
+    nb = sum(used)
+    table = torch.full((n, width), -1, dtype=torch.int32)
+    ids, at = torch.randperm(nb, generator=torch.Generator().manual_seed(2)), 0
+    for b, u in enumerate(used):
+        table[b, :u] = ids[at:at + u]
+        at += u
+    table = table.cuda()
+    lens = [torch.tensor([c + 1 + i for c in first], dtype=torch.int32,
+                         device="cuda") for i in range(steps)]
+    shape = (nb, hkv, bs, d)
+    dt = torch.bfloat16
+    pool0 = [torch.randn(shape, generator=g, device="cuda").to(
+        E4M3 if q8 else dt) for _ in "kv"]
+    if q8:
+        pool0 += [torch.full((nb, hkv), 2.0 ** -6, device="cuda")
+                  for _ in "kv"]
+    rows = [(torch.randn(n, hq + 2 * hkv, d, generator=g, device="cuda") *
+             2.0 ** i).to(dt) for i in range(steps)]
+    append = pkv.pa_append_q8 if q8 else pkv.pa_append
+    decode = pkv.pa_decode_q8 if q8 else pkv.pa_decode
+    assert pkv.pa_decode_partition_size(
+        pkv.make_desc(rows[0][:, :hq], pool0[0], table)) == 4096
+
+    def run(sync):
+        pool = [p.clone() for p in pool0]
+        q = torch.empty(n, hq, d, dtype=dt, device="cuda")
+        outs = [torch.empty(n, hq, d, dtype=dt, device="cuda")
+                for _ in range(steps)]
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        if not sync:
+            torch.cuda._sleep(4_000_000)  # the calls below are queued behind
+        for x, length, out in zip(rows, lens, outs):
+            append(q, *pool, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:],
+                   table, length, dev_err=err)
+            if sync:
+                torch.cuda.synchronize()
+            decode(out, q, *pool, table, length, d ** -0.5, workspace=ws,
+                   dev_err=err)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        return outs + [p.view(torch.uint8) for p in pool] + [q]
+
+    want = run(True)
+    assert torch.isfinite(torch.stack(want[:steps]).float()).all()
+    for _ in range(10):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
