@@ -149,8 +149,12 @@ const char* pa_last_error(void);
  * the decode, and with more than 16 partitions or PA_REDUCE_KERNEL the
  * reduce kernel, chained by programmatic dependent launch.  The prep kernel
  * reads context_lens before it waits for the kernel launched just before
- * the call, so that kernel, if it lets its dependents start early, must
- * not be the one that writes context_lens.
+ * the call.  So a kernel that writes context_lens and lets its dependents
+ * start early must have completed when this call's first kernel may start:
+ * it must not be the one just before the call, nor stand before it with
+ * nothing but attention calls (pa_decode, pa_prefill, their _q8 forms)
+ * between, which also start early.  The library's other kernels start their
+ * successors only once all earlier work of the stream has completed.
  * Computation: fp32 scores, fp32 online softmax, fp32 accumulation; the
  * output is rounded once to dtype.
  * Errors: PA_ERR_INVALID_ARG / PA_ERR_UNSUPPORTED / PA_ERR_WORKSPACE before
@@ -307,9 +311,8 @@ size_t pa_prefill_workspace_bytes(const pa_prefill_desc* desc);
  * loads its next item while it computes the current one.
  * PA_ERR_UNSUPPORTED when the items would exceed 2^31 - 1.  The first kernel is itself
  * launched programmatically: it reads context_lens and query_start before
- * it waits for the kernel launched just before the call, so that kernel,
- * if it lets its dependents start early, must not be the one that writes
- * them. */
+ * it waits for the kernel launched just before the call, so pa_decode's
+ * rule on the kernel that writes context_lens holds for both. */
 pa_status pa_prefill(void* out, const void* q, const void* k_cache,
                      const void* v_cache, const int32_t* block_tables,
                      const int32_t* context_lens, const int32_t* query_start,

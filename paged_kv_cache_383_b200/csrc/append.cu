@@ -576,8 +576,10 @@ __global__ void __launch_bounds__(kThreads, kQ8 ? 3 : 4)
   // cos/sin: the pairs of the CTA's tokens, or of a block's.
   __shared__ __align__(16) float2
       cs[(kQ8 ? kMaxBlock : kMaxTokens) * kTokenStride];
-  dev::pdl_trigger();  // a following attention may run its prologue now
-  dev::pdl_wait();     // q, k and v may be the previous kernel's output
+  dev::pdl_wait();  // q, k and v may be the previous kernel's output
+  // A following attention may run its prologue now.  Not before the wait: it
+  // reads lengths, which a kernel before this one may still be writing.
+  dev::pdl_trigger();
   if (kQ8 && static_cast<int>(blockIdx.x) < a.kv_ctas) {
     window_kv<T, D>(a, blockIdx.x / a.unit_groups, blockIdx.x % a.unit_groups,
                     cs);

@@ -32,8 +32,10 @@ __global__ void __launch_bounds__(kThreads)
                           const int32_t* __restrict__ pairs,
                           int64_t block_chunks, int num_kv_heads, int num_src,
                           int num_dst, int32_t* dev_err) {
-  dev::pdl_trigger();  // a following attention may run its prologue now
   dev::pdl_wait();
+  // A following attention may run its prologue now.  Not before the wait: it
+  // reads lengths, which a kernel before this one may still be writing.
+  dev::pdl_trigger();
   const int32_t s = pairs[2 * blockIdx.x];
   const int32_t d = pairs[2 * blockIdx.x + 1];
   if (s < 0 || s >= num_src || d < 0 || d >= num_dst) {

@@ -6,6 +6,8 @@ sources: a race cannot be shown by running it."""
 import os
 import re
 
+import pytest
+
 from conftest import ROOT
 
 CSRC = os.path.join(ROOT, "paged_kv_cache_383_b200", "csrc")
@@ -32,3 +34,15 @@ def test_reduce_waits_before_it_leaves():
     code = body(source("decode_common.cuh"), "reduce_kernel")
     assert "return" in code
     assert code.index("pdl_wait") < code.index("return")
+
+
+@pytest.mark.parametrize("name,kernel", [
+    ("append.cu", "append_kernel"), ("cache_ops_q8.cu", "move_blocks_q8_kernel")])
+def test_writers_release_their_successors_after_waiting(name, kernel):
+    """An attention call behind these reads its lengths before its own wait:
+    they must not let it start while a kernel before them (the writer of the
+    lengths, say) still runs."""
+    code = body(source(name), kernel)
+    assert code.index("pdl_wait") < code.index("pdl_trigger")
+    head = code[:code.index("pdl_trigger")]
+    assert "return" not in head and "if" not in head
