@@ -447,17 +447,17 @@ def _code(dt) -> int:
 
 
 def _workspace(need: int, device, stream):
-    """A workspace of the call's own.  torch hands its memory out again on
-    the stream it was allocated on, so one used on another stream is marked
-    as in use there."""
-    ws = _tc["empty"](max(need, 16), dtype=_tc["u8"], device=device)
-    if stream is not None:
-        import torch
-        s = torch.cuda.ExternalStream(stream, device=device) \
-            if isinstance(stream, int) else stream
-        if s != torch.cuda.current_stream():
-            ws.record_stream(s)
-    return ws
+    """A workspace of the call's own, out of the memory that torch keeps for
+    the stream the call runs on.  Memory of another stream's would not do:
+    torch hands it out as soon as that stream's last user is queued, and that
+    user may still be running when this call starts."""
+    if stream is None:
+        return _tc["empty"](max(need, 16), dtype=_tc["u8"], device=device)
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return _tc["empty"](max(need, 16), dtype=_tc["u8"], device=device)
 
 
 def _check_q8(k_cache, v_cache, k_scales, v_scales, names=("", "")):

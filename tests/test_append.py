@@ -301,3 +301,27 @@ def test_oracle_scale_and_rotation():
         z = oap.rotate_head(oap.rotate_head(x, 45, f, layout, 1.0), 12300, f,
                             layout, 1.0)
         np.testing.assert_allclose(y, z, atol=1e-9)
+
+
+def test_workspace_belongs_to_the_stream_it_is_used_on(pkv, monkeypatch):
+    """Allocated while another stream is current, it could be memory that a
+    call queued there still uses."""
+    import contextlib
+
+    import torch
+    current, at = ["caller's"], []
+
+    @contextlib.contextmanager
+    def use(stream):
+        current.append(stream)
+        yield
+        current.pop()
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda handle, device=None: ("handle", handle))
+    pkv._torch_refs()
+    monkeypatch.setitem(pkv._tc, "empty",
+                        lambda *a, **k: at.append(current[-1]))
+    for stream in (None, "side", 77):
+        pkv._workspace(64, "cuda:0", stream)
+    assert at == ["caller's", "side", ("handle", 77)]

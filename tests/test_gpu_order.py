@@ -71,3 +71,65 @@ def test_decode_then_append_of_the_next_step(pkv, q8):
     for _ in range(10):
         for a, b in zip(run(False), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_calls_on_two_streams_without_a_workspace(pkv, handle):
+    """A long call on the current stream and, without any wait between them, a
+    call on a stream of its own: neither is given a workspace, so each must
+    have memory of its own."""
+    hq, hkv, d, bs = 32, 8, 128, 16
+    torch.manual_seed(3)
+    sets = []
+    for lens in ([30_000, 9_000, 500, 20_000], [700, 25_000, 16_000, 3]):
+        used = [-(-n // bs) for n in lens]
+        nb = sum(used)
+        table = torch.zeros(4, max(used), dtype=torch.int32)
+        ids, at = torch.randperm(nb), 0
+        for b, u in enumerate(used):
+            table[b, :u] = ids[at:at + u]
+            at += u
+        pool = [torch.randn(nb, hkv, bs, d, device="cuda").to(E4M3)
+                for _ in "kv"]
+        pool += [torch.rand(nb, hkv, device="cuda") + 0.5 for _ in "kv"]
+        q = torch.randn(40, hq, d, device="cuda").bfloat16()
+        sets.append((q, pool, table.cuda(),
+                     torch.tensor(lens, dtype=torch.int32, device="cuda")))
+    start = torch.tensor([0, 20, 30, 39, 40], dtype=torch.int32,
+                         device="cuda")
+
+    def call(out, x, kind, stream):
+        q, pool, table, lens = x
+        if kind == "decode":
+            pkv.pa_decode_q8(out, q[:4], *pool, table, lens, 0.09,
+                             partition_size=64, stream=stream)
+        else:
+            pkv.pa_prefill_q8(out, q, *pool, table, lens, start, 0.09,
+                              max_q_len=20, stream=stream)
+
+    def outs(kind, n):
+        return [torch.empty(4 if kind == "decode" else 40, hq, d,
+                            dtype=torch.bfloat16, device="cuda")
+                for _ in range(n)]
+
+    want = {}
+    for kind in ("decode", "prefill"):
+        want[kind] = outs(kind, 2)
+        for out, x in zip(want[kind], sets):
+            call(out, x, kind, None)
+            torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for kind in ("decode", "prefill"):
+            got = outs(kind, 4)
+            torch.cuda.synchronize()
+            torch.cuda._sleep(1_000_000)  # both streams start together
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(1_000_000)
+            for i, out in enumerate(got):
+                s = None if i % 2 == 0 else side.cuda_stream if handle \
+                    else side
+                call(out, sets[i % 2], kind, s)
+            torch.cuda.synchronize()
+            for i, out in enumerate(got):
+                assert torch.equal(out, want[kind][i % 2])
