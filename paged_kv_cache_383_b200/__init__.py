@@ -179,7 +179,8 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     _out_mode(desc, out, dt)
     need = int(lib.pa_decode_workspace_bytes(ctypes.byref(desc)))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _tc or _torch_refs()
+        workspace = _workspace(need, q.device, stream)
     ws_ptr = _dev(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() \
         if workspace is not None else 0
@@ -278,8 +279,8 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, context_lens,
     _out_mode(desc, out, q.dtype)
     need = lib.pa_prefill_workspace_bytes(ctypes.byref(desc))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8,
-                                device=q.device)
+        _tc or _torch_refs()
+        workspace = _workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     st = lib.pa_prefill(
         _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"),

@@ -325,3 +325,25 @@ def test_workspace_belongs_to_the_stream_it_is_used_on(pkv, monkeypatch):
     for stream in (None, "side", 77):
         pkv._workspace(64, "cuda:0", stream)
     assert at == ["caller's", "side", ("handle", 77)]
+
+
+def test_16_bit_attention_takes_its_workspace_the_same_way(pkv, monkeypatch):
+    import torch
+    asked = []
+
+    def workspace(need, device, stream):
+        asked.append((need, stream))
+        raise KeyboardInterrupt
+    monkeypatch.setattr(pkv, "_workspace", workspace)
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(5, 2, 16, 64, dtype=torch.bfloat16)
+    table = torch.zeros(2, 3, dtype=torch.int32)
+    lens = torch.zeros(2, dtype=torch.int32)
+    start = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(KeyboardInterrupt):
+        pkv.pa_decode(q, q, kc, kc, table, lens, 0.1, stream="side")
+    with pytest.raises(KeyboardInterrupt):
+        pkv.pa_prefill(q, q, kc, kc, table, lens, start, 0.1, max_q_len=1,
+                       stream="side")
+    assert [s for _, s in asked] == ["side", "side"]
+    assert all(n > 0 for n, _ in asked)

@@ -74,7 +74,8 @@ def test_decode_then_append_of_the_next_step(pkv, q8):
 
 
 @pytest.mark.parametrize("handle", [False, True])
-def test_calls_on_two_streams_without_a_workspace(pkv, handle):
+@pytest.mark.parametrize("q8", [False, True])
+def test_calls_on_two_streams_without_a_workspace(pkv, q8, handle):
     """A long call on the current stream and, without any wait between them, a
     call on a stream of its own: neither is given a workspace, so each must
     have memory of its own."""
@@ -89,9 +90,10 @@ def test_calls_on_two_streams_without_a_workspace(pkv, handle):
         for b, u in enumerate(used):
             table[b, :u] = ids[at:at + u]
             at += u
-        pool = [torch.randn(nb, hkv, bs, d, device="cuda").to(E4M3)
-                for _ in "kv"]
-        pool += [torch.rand(nb, hkv, device="cuda") + 0.5 for _ in "kv"]
+        pool = [torch.randn(nb, hkv, bs, d, device="cuda").to(
+            E4M3 if q8 else torch.bfloat16) for _ in "kv"]
+        if q8:
+            pool += [torch.rand(nb, hkv, device="cuda") + 0.5 for _ in "kv"]
         q = torch.randn(40, hq, d, device="cuda").bfloat16()
         sets.append((q, pool, table.cuda(),
                      torch.tensor(lens, dtype=torch.int32, device="cuda")))
@@ -101,11 +103,13 @@ def test_calls_on_two_streams_without_a_workspace(pkv, handle):
     def call(out, x, kind, stream):
         q, pool, table, lens = x
         if kind == "decode":
-            pkv.pa_decode_q8(out, q[:4], *pool, table, lens, 0.09,
-                             partition_size=64, stream=stream)
+            fn = pkv.pa_decode_q8 if q8 else pkv.pa_decode
+            fn(out, q[:4], *pool, table, lens, 0.09, partition_size=64,
+               stream=stream)
         else:
-            pkv.pa_prefill_q8(out, q, *pool, table, lens, start, 0.09,
-                              max_q_len=20, stream=stream)
+            fn = pkv.pa_prefill_q8 if q8 else pkv.pa_prefill
+            fn(out, q, *pool, table, lens, start, 0.09, max_q_len=20,
+               stream=stream)
 
     def outs(kind, n):
         return [torch.empty(4 if kind == "decode" else 40, hq, d,
