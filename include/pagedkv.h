@@ -497,8 +497,10 @@ pa_status pa_rope_freqs(const pa_rope_desc* desc, double* freqs_out,
  * keeps its relative precision (2^-4) over 15 binades, so the scales that
  * pa_append_q8 chooses are powers of two: nothing is lost against others,
  * and codes that follow a grown scale move exactly unless they become
- * subnormal.  Attention accepts any positive finite scales (2^-100 to 2^100;
- * a scale of 0 stands for a block of zeros).
+ * subnormal.  Attention accepts any positive finite scales from 2^-100 on, and
+ * 0, which stands for a block of zeros; as over the 16-bit cache, the weighted
+ * sum of the values before its division by the weights' sum must be finite in
+ * float32.
  *
  * pa_append_q8 -- pa_append into this cache.  For a block and head of which
  * the call writes slots o .. o + m - 1 (always a run), with A the largest

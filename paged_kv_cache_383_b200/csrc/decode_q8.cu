@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, ctas_q8(BS))
     // Online softmax; this lane holds heads 2*t4 and 2*t4+1.  o also
     // follows E, the running exponent of vs.
     float o_scale = 1.f;
-    const int e_vs = max(-100, min(100, dev::floor_log2(vs)));
+    // -100 and 127 keep E - 10 and 10 - E in exp2_int's range.
+    const int e_vs = max(-100, min(127, dev::floor_log2(vs)));
     if (e_vs > e_run + 3) {  // the same in every lane
       o_scale = dev::exp2_int(max(e_run - e_vs, -126));
       e_run = e_vs;

@@ -447,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int group = t / kGroup;
             if (group + 1 < groups) next = fetch(group + 1, id2);
             if (group + 2 < groups) id2 = fetch_id(group + 2);
-            lv = fminf(fmaxf(log2f(cur.vs), -100.f), 100.f);
+            // -100 keeps E - kShift in exp2_int's range (at the top it is: a
+            // float's log2 ends at 128).  A scale of 0: no weight at all.
+            lv = cur.vs > 0.f ? fmaxf(log2f(cur.vs), -100.f) : -1000.f;
             top = lv;  // the largest of each tile's pages
 #pragma unroll
             for (int m = 1; m < kNB; m <<= 1)
@@ -457,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t id = __shfl_sync(0xffffffffu, cur.id, from);
           const float ks = __shfl_sync(0xffffffffu, cur.ks, from);
           const float my_lv = __shfl_sync(0xffffffffu, lv, from);
-          const int e_top = static_cast<int>(
-              floorf(__shfl_sync(0xffffffffu, top, in * kNB)));
+          const int e_top = static_cast<int>(fmaxf(
+              floorf(__shfl_sync(0xffffffffu, top, in * kNB)), -100.f));
           if (t == 0 || e_top > e_ref + kVsSlack) e_ref = e_top;
           // A slot is written again kScaleSlots tiles on.  K tile t is copied
           // at most kRaw tiles ahead of the one being converted, which is at

@@ -1,0 +1,103 @@
+"""The 8-bit cache at the ends of its scales' range, and NaN in its parts."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_q8 import (BF, E4M3, HF, Pool, bound_prefill, decode, positions,
+                         prefill, reference, to64)
+
+pytestmark = pytest.mark.gpu
+
+
+def both(pkv, pool, q, start, scale, max_q_len):
+    """float32 outputs of the prefill, and of the decode of each sequence's
+    last row, with the fp64 reference and the error allowed to each element
+    (bound_prefill's terms cover the decode: its weights are fp16 too, kept
+    relative to the largest v scale)."""
+    new = np.diff(start)
+    pos = positions(pool.ctx.tolist(), new.tolist())
+    ref, mag = reference(pool, q, pos, scale)
+    tol = bound_prefill(pool, q, pos, scale, mag)
+    last = torch.from_numpy(np.asarray(start[1:]) - 1).cuda()
+    p32, p16 = prefill(pkv, pool, q, start, scale, max_q_len)
+    d32, d16 = decode(pkv, pool, q[last].contiguous(), scale)
+    assert torch.equal(p16, p32.to(q.dtype))
+    assert torch.equal(d16, d32.to(q.dtype))
+    last = last.cpu().numpy()
+    return (p32, ref, tol), (d32, ref[last], tol[last])
+
+
+@pytest.mark.parametrize("exp", [120, 113, 104, 101, 60, -60, -64, -90])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_scales_of_any_size(pkv, exp, mixed):
+    """V scales around 2^exp (one of 2^120 is what an append of the largest
+    bf16 values writes), with and without much smaller ones beside them, the
+    small ones first.  Codes are small enough that sums fit float32."""
+    ctx, new = [1, 40, 100, 70], [1, 30, 2, 70]
+    pool = Pool(2, 128, 16, ctx, seed=5)
+    codes = pool.vc.float()
+    pool.vc.copy_((codes / 448 if exp > 110 else codes).to(E4M3))
+    ok = ~torch.isnan(pool.vs)
+    e = torch.full_like(pool.vs, float(exp))
+    if mixed:
+        for row in pool.table:
+            for i, blk in enumerate(row[row >= 0]):
+                e[int(blk)] = exp - 30 + 10 * i if i < 3 else exp - i % 2
+    pool.vs.copy_(torch.where(ok, torch.exp2(e.clamp_(-100, 120)), pool.vs))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(sum(new), 8, 128, generator=g, device="cuda").to(BF)
+    start = np.concatenate([[0], np.cumsum(new)])
+    for out, ref, tol in both(pkv, pool, q, start, 0.09, 70):
+        assert (np.abs(to64(out) - ref) <= tol).all(), \
+            float((np.abs(to64(out) - ref) / tol).max())
+
+
+def test_large_values_come_back(pkv):
+    """bf16 values up to the largest whose code still stands for a float32,
+    appended and attended to: a context of one token returns what the code
+    stands for."""
+    rows = torch.randn(7, 2, 64, device="cuda") * 2.0 ** torch.tensor(
+        [0., 60., 100., 110., 115., 120., 125.], device="cuda")[:, None, None]
+    rows = rows.to(BF)
+    rows[6, :, :2] = torch.tensor([3.2e38, -3.2e38], device="cuda").to(BF)
+    table = torch.arange(7, dtype=torch.int32, device="cuda")[:, None]
+    table = table.contiguous()
+    lens = torch.ones(7, dtype=torch.int32, device="cuda")
+    z = torch.zeros(7, 2, 16, 64, device="cuda").to(E4M3)
+    cache = [z, z.clone()] + [torch.zeros(7, 2, device="cuda") for _ in "kv"]
+    keys = torch.randn(7, 2, 64, device="cuda").to(BF)
+    pkv.pa_append_q8(None, *cache, None, keys, rows, table, lens)
+    assert float(cache[3].max()) == 2.0 ** 120
+    want = to64(cache[1])[:, :, 0] * to64(cache[3])[:, :, None]
+    assert (np.abs(want - to64(rows)) <= np.abs(to64(rows)) * 2.0 ** -4 +
+            to64(cache[3])[:, :, None] * 2.0 ** -10).all()
+    q = torch.randn(7, 4, 64, device="cuda").to(BF)
+    start = torch.arange(8, dtype=torch.int32, device="cuda")
+    outs = [torch.empty(7, 4, 64, device="cuda") for _ in "12"]
+    pkv.pa_decode_q8(outs[0], q, *cache, table, lens, 0.125)
+    pkv.pa_prefill_q8(outs[1], q, *cache, table, lens, start, 0.125,
+                      max_q_len=1)
+    # one weight, 1, which fp16 holds: what is left is the exponential's
+    # argument in fp32, 2^-15 of the sum that divides
+    for out in outs:
+        got = to64(out).reshape(7, 2, 2, 64)
+        assert (np.abs(got - want[:, :, None]) <=
+                2.0 ** -15 * np.abs(want[:, :, None])).all()
+
+
+def test_zero_scales_give_zeros(pkv):
+    """Blocks of scale 0 count as zeros whatever their codes, alone or beside
+    blocks of the smallest scales."""
+    ctx, new = [33, 48, 130], [33, 1, 4]
+    for tiny in (False, True):
+        pool = Pool(2, 64, 16, ctx, seed=7)
+        for b, row in enumerate(pool.table):
+            for i, blk in enumerate(row[row >= 0]):
+                pool.vs[int(blk)] = 2.0 ** -100 if tiny and i % 2 else 0.0
+        q = torch.randn(sum(new), 8, 64, device="cuda").to(HF)
+        start = np.concatenate([[0], np.cumsum(new)])
+        for out, ref, tol in both(pkv, pool, q, start, 0.125, 33):
+            if tiny:  # values of 2^-91 and less: the bound's own floor aside
+                assert (np.abs(to64(out) - ref) <= tol - 1e-30 + 1e-38).all()
+            else:
+                assert (out == 0).all()
