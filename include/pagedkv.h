@@ -500,7 +500,7 @@ pa_status pa_rope_freqs(const pa_rope_desc* desc, double* freqs_out,
  * subnormal.  Attention accepts any positive finite scales from 2^-100 on, and
  * 0, which stands for a block of zeros; as over the 16-bit cache, the weighted
  * sum of the values before its division by the weights' sum must be finite in
- * float32.
+ * float32.  A NaN scale gives NaN to the rows that see a token of its block.
  *
  * pa_append_q8 -- pa_append into this cache.  For a block and head of which
  * the call writes slots o .. o + m - 1 (always a run), with A the largest

@@ -179,6 +179,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
       return false;
   }
 }
+constexpr float kTiny = 1.1754944e-38f;  // the smallest normal float
+
+// The larger of the two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // One arrival for a converged warp, without a branch.  (What it publishes is
 // ordered by the caller: a warp-wide tcgen05 wait, or __syncwarp.)
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
@@ -457,7 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int from = in * kNB + (lane < kNB ? lane : 0);
           const int32_t id = __shfl_sync(0xffffffffu, cur.id, from);
-          const float ks = __shfl_sync(0xffffffffu, cur.ks, from);
+          // (a NaN scale, of K or of V, makes its block's scores NaN)
+          const float ks =
+              __shfl_sync(0xffffffffu, cur.ks + 0.f * cur.vs, from);
           const float my_lv = __shfl_sync(0xffffffffu, lv, from);
           const int e_top = static_cast<int>(fmaxf(
               floorf(__shfl_sync(0xffffffffu, top, in * kNB)), -100.f));
@@ -841,19 +852,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int tile = first + j * sp.stride;
       const int lim = qpos - tile * kKeys;  // the last key this row sees
+      // A factor c_row ks_b for each block (never 0: -inf * 0 is NaN).
+      const float* sc = scale_s + ((g + tile) % kScaleSlots) * kSlotFloats;
+      float cb[kNB];
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) cb[b] = max_nan(c_row * sc[b], kTiny);
       if (lim < kKeys - 1) {
 #pragma unroll
         for (int k = 0; k < kKeys; ++k)
           if (k > lim) sv[k] = -INFINITY;
+        // nor does a NaN scale reach a row that sees nothing of its block
+#pragma unroll
+        for (int b = 0; b < kNB; ++b)
+          if (b * BS > lim) cb[b] = kTiny;
       }
-      // The row's maximum, by blocks: a factor c_row ks_b for each (never 0:
-      // -inf * 0 is NaN).
-      const float* sc = scale_s + ((g + tile) % kScaleSlots) * kSlotFloats;
-      float cb[kNB];
+      // The row's maximum, by blocks.
       float mx = -INFINITY;
 #pragma unroll
       for (int b = 0; b < kNB; ++b) {
-        cb[b] = fmaxf(c_row * sc[b], 1.1754944e-38f);
         float m4[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {

@@ -101,3 +101,23 @@ def test_zero_scales_give_zeros(pkv):
                 assert (np.abs(to64(out) - ref) <= tol - 1e-30 + 1e-38).all()
             else:
                 assert (out == 0).all()
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("new", [70, 4])
+def test_nan_scale_reaches_the_rows_that_see_its_block(pkv, which, new):
+    """The scale of positions 304 .. 319 of the first context."""
+    ctx = [330, 330]
+    pool = Pool(2, 128, 16, ctx, seed=3)
+    blk, first = int(pool.table[0, 19]), 304
+    (pool.ks if which == "k" else pool.vs)[blk, 1] = float("nan")
+    q = torch.randn(2 * new, 8, 128, device="cuda").to(HF)
+    start = [0, new, 2 * new]
+    out, _ = prefill(pkv, pool, q, start, 0.09, new)
+    pos = torch.arange(330 - new, 330, device="cuda")
+    hit = torch.zeros(2 * new, 8, dtype=torch.bool, device="cuda")
+    hit[:new, 4:] = (pos >= first)[:, None]
+    assert torch.equal(torch.isnan(out), hit[..., None].expand_as(out))
+    last, _ = decode(pkv, pool, q[[new - 1, 2 * new - 1]].contiguous(), 0.09)
+    assert torch.isnan(last[0, 4:]).all()
+    assert torch.isfinite(last[0, :4]).all() and torch.isfinite(last[1]).all()
