@@ -543,7 +543,8 @@ pa_status pa_decode_q8(void* out, const void* q, const void* k_cache,
 /* pa_prefill over the 8-bit cache: the same descriptor (dtype is that of q
  * and out; kernel and pv are checked but change nothing: the weights are
  * fp16, which needs no residual), workspace (pa_prefill_workspace_bytes),
- * launches, checks and errors.  Any scale sign; sizes as pa_prefill. */
+ * launches, checks and errors.  `scale` may have any sign; sizes as
+ * pa_prefill.  A NaN code reaches the rows that see its token only. */
 pa_status pa_prefill_q8(void* out, const void* q, const void* k_cache,
                         const void* v_cache, const float* k_scales,
                         const float* v_scales, const int32_t* block_tables,

@@ -75,12 +75,13 @@ constexpr int kThreads = 16 * 32;  // whole warpgroups; warp 15 has no work
 // (a softmax thread holds 64 scores).  The sum must not exceed the launch's:
 // an increase waits for registers that the others gave up.
 constexpr int kLaunchRegs = 128;
-constexpr int kSoftmaxRegs = 192, kConvRegs = 48, kIssueRegs = 80;
+constexpr int kSoftmaxRegs = 192, kConvRegs = 56, kIssueRegs = 72;
 static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs == 4 * kLaunchRegs,
               "more registers than the block was launched with");
 // What the page warp stages for a tile: for each of its blocks ks, the
 // exponent log2(vs) - E + kShift and 2^-that; and E, last.
 constexpr int kSlotFloats = 16;
+constexpr int kNanSlots = 8, kNanInts = 8;
 // Tensor memory columns, for each query tile: S 64, P 32, the last 64 dims of
 // q 32, O head_dim (up to 128).
 constexpr int kTmemCols = 512;
@@ -136,7 +137,9 @@ struct LayoutQ8 {
   static constexpr int kOffScales = kOffRaw + 2 * kRaw * kRawTile;
   // maximum, sum and E of each row of query tile 1, for its merge with tile 0
   static constexpr int kOffMerge = kOffScales + kScaleSlots * kSlotFloats * 4;
-  static constexpr int kOffBars = kOffMerge + 3 * kRows * 4;
+  // of kNanSlots items in turn: kNanInts ints (see the converters)
+  static constexpr int kOffNan = kOffMerge + 3 * kRows * 4;
+  static constexpr int kOffBars = kOffNan + kNanSlots * kNanInts * 4;
   static constexpr size_t kSmemBytes =
       1024 + kOffBars + kNumBars * 8 + 16 + 2 * kItemWords * 4;
 };
@@ -186,6 +189,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// 0xff for each byte of w that is a NaN code (0x7f, 0xff), 0 for the others.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  const uint32_t n = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return 2u * n - (n >> 7);
 }
 
 // One arrival for a converged warp, without a branch.  (What it publishes is
@@ -280,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     dev::fence_mbar_init();
   }
+  int* nan_s = reinterpret_cast<int*>(smem + Lay::kOffNan);
+  if (tid < kNanSlots) nan_s[kNanInts * tid] = 0;
   if (warp == kMmaWarp) {
     dev::tmem_alloc(dev::smem_u32(tmem_slot), kTmemCols);
     dev::tmem_relinquish();
@@ -656,9 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0;
     bool ok = true;
     // Tile t of K (w = 0) or V (w = 1) into its stage, once the one before
-    // there was read; rows from `limit` on become zeros (a key past the context
-    // has weight 0, but 0 * NaN is NaN in the MMA).
-    auto convert = [&](int w, uint32_t t, int limit) -> bool {
+    // there was read.  Of a V tile that some row of the item sees in part, what
+    // would reach that row with its weight of 0 becomes zero, as 0 * NaN is NaN
+    // in the MMA: rows from `limit` on, the context's end, and NaN codes; if
+    // there were any of these, *nan_flag is set.
+    auto convert = [&](int w, uint32_t t, bool partly, int limit,
+                       int* nan_flag) -> bool {
       const uint32_t slot = w * kRaw + t % kRaw, s = t % kStages;
       if (!warp_wait(raw_full0 + 8 * slot, (t / kRaw) & 1) ||
           (t >= kStages && !warp_wait((w ? v_empty0 : k_empty0) + 8 * s,
@@ -667,11 +681,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint8_t* raw = smem + Lay::kOffRaw + slot * Lay::kRawTile +
                            row0 * D + cc * 16;
       uint8_t* d = smem + (w ? Lay::kOffV : Lay::kOffK) + s * Lay::kTile;
-      auto chunk = [&](int row_step, int half, bool zero) {
-        uint4 w = *reinterpret_cast<const uint4*>(raw + row_step * D +
-                                                  half * 64);
-        if (zero) w = make_uint4(0u, 0u, 0u, 0u);
-        uint8_t* to = d + half * kTileHalf + row_step * 128;
+      auto load = [&](int i) {
+        return *reinterpret_cast<const uint4*>(
+            raw + 32 * (i / kHalves) * D + ((i % kHalves) ^ flip) * 64);
+      };
+      auto store = [&](int i, const uint4& w) {
+        uint8_t* to = d + ((i % kHalves) ^ flip) * kTileHalf +
+                      32 * (i / kHalves) * 128;
         *reinterpret_cast<uint4*>(to + e0) = make_uint4(
             dev::e4m3x2_to_f16x2(w.x), dev::e4m3x2_to_f16x2_hi(w.x),
             dev::e4m3x2_to_f16x2(w.y), dev::e4m3x2_to_f16x2_hi(w.y));
@@ -679,15 +695,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::e4m3x2_to_f16x2(w.z), dev::e4m3x2_to_f16x2_hi(w.z),
             dev::e4m3x2_to_f16x2(w.w), dev::e4m3x2_to_f16x2_hi(w.w));
       };
-      if (limit >= kKeys) {
+      if (!partly) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          chunk(32 * (i / kHalves), (i % kHalves) ^ flip, false);
+        for (int i = 0; i < kPer; ++i) store(i, load(i));
       } else {
+        uint32_t nans = 0u;
 #pragma unroll 1
-        for (int i = 0; i < kPer; ++i)
-          chunk(32 * (i / kHalves), (i % kHalves) ^ flip,
-                row0 + 32 * (i / kHalves) >= limit);
+        for (int i = 0; i < kPer; ++i) {
+          uint4 w = load(i);
+          if (row0 + 32 * (i / kHalves) >= limit)
+            w = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 n = make_uint4(nan_bytes(w.x), nan_bytes(w.y),
+                                     nan_bytes(w.z), nan_bytes(w.w));
+          nans |= n.x | n.y | n.z | n.w;
+          store(i, make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z,
+                              w.w & ~n.w));
+        }
+        if (nans) *nan_flag = 1;
       }
       dev::fence_proxy_async_smem();  // visible to the tensor cores
       __syncwarp();
@@ -699,12 +723,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item it;
       ok = next_item(n, it);
       if (!ok || it.state == kEnd) break;
+      // NaN codes that are taken out belong to the rows that see them: the
+      // item's slot (flag, sequence, KV head, first key, row of position 0)
+      // tells the epilogue to look for them.  Its flag is cleared four items ahead: an item is
+      // published once every warp has taken up the one two before, so the
+      // slot's last readers (of eight items back) are done when it is cleared,
+      // and it is clear when its first writer comes.
+      int* nan_at = nan_s + kNanInts * (n % kNanSlots);
+      if (ctid == 0) nan_s[kNanInts * ((n + 4) % kNanSlots)] = 0;
       if (it.state == kSkip) continue;
       const Span sp = span_of(it);
+      const int seen = it.L - it.q_len + sp.tok0[0] + 1;  // by every row
+      if (ctid == 0) {
+        nan_at[1] = it.b;
+        nan_at[2] = it.kvh;
+        nan_at[3] = seen / kKeys * kKeys;
+        nan_at[4] = it.q0 + it.q_len - it.L;
+      }
       for (int t = 0; ok && t <= sp.tiles; ++t) {
-        if (t < sp.tiles) ok = convert(0, g + t, kKeys);
+        if (t < sp.tiles) ok = convert(0, g + t, false, 0, nullptr);
         if (ok && t >= 1)
-          ok = convert(1, g + t - 1, it.L - (t - 1) * kKeys);
+          ok = convert(1, g + t - 1, t * kKeys > seen,
+                       it.L - (t - 1) * kKeys, nan_at);
       }
       g += sp.tiles;
     }
@@ -1029,6 +1069,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       dev::tc_fence_before();
+      // Rare: the NaN codes that the converters took out, back into the
+      // outputs of the row that sees them.
+      const volatile int* nan_at = nan_s + kNanInts * (n % kNanSlots);
+      if (nan_at[0] != 0 && valid) {
+        const int64_t row =
+            (static_cast<int64_t>(nan_at[4] + qpos) * a.num_q_heads +
+             nan_at[2] * G + hg) * D;
+#pragma unroll 1
+        for (int key = nan_at[3]; key <= qpos; ++key) {
+          const int32_t id =
+              a.block_tables[static_cast<int64_t>(nan_at[1]) *
+                                 a.max_blocks_per_seq + key / BS];
+          if (id < 0 || id >= a.num_blocks) continue;  // flagged already
+          const uint8_t* codes =
+              a.v_cache + ((static_cast<int64_t>(id) * a.num_kv_heads +
+                            nan_at[2]) * BS + key % BS) * D;
+#pragma unroll 1
+          for (int i = 0; i < D; ++i) {
+            if ((codes[i] & 0x7f) != 0x7f) continue;
+            if (a.out_f32)
+              static_cast<float*>(a.out)[row + i] = NAN;
+            else
+              static_cast<uint16_t*>(a.out)[row + i] =
+                  static_cast<uint16_t>(dev::Mma<T>::pack(NAN, NAN));
+          }
+        }
+      }
     }
     if (ok && sp.stride == 2 && x == 0) {
       __syncwarp();

@@ -121,3 +121,40 @@ def test_nan_scale_reaches_the_rows_that_see_its_block(pkv, which, new):
     last, _ = decode(pkv, pool, q[[new - 1, 2 * new - 1]].contiguous(), 0.09)
     assert torch.isnan(last[0, 4:]).all()
     assert torch.isfinite(last[0, :4]).all() and torch.isfinite(last[1]).all()
+
+
+@pytest.mark.parametrize("group,new,bs", [
+    (1, 150, 16), (8, 150, 32), (4, 70, 16), (8, 8, 16), (1, 1, 32)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_values_reach_the_rows_that_see_them(pkv, group, new, bs, d):
+    """NaN V codes of new and of old tokens: each makes its dim NaN in the
+    rows from its position on, whichever tile they are computed in, and
+    changes nothing else."""
+    ctx = [330, 200, 330]
+    new = [new, min(new, 200), new]
+    pool = Pool(2, d, bs, ctx, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(group)
+    q = torch.randn(sum(new), 2 * group, d, generator=g, device="cuda").to(BF)
+    start = np.concatenate([[0], np.cumsum(new)])
+    clean, _ = prefill(pkv, pool, q, start, 0.09, max(new))
+    bad = np.full((3, 2, d), 1 << 30)   # first NaN key by dim
+    raw = pool.vc.view(torch.uint8)
+    keys = {0: (0, 63, 64, 181, 200, 250, 255, 256, 300, 329, 329),
+            2: (5, 187, 191, 192, 319, 320, 321, 328)}
+    for b, at in keys.items():
+        for i, p in enumerate(at):
+            if p < ctx[b] - new[b] and i % 3:
+                continue                # a few old tokens only
+            h, e = i % 2, (7 * i + 3 * b) % d
+            raw[int(pool.table[b, p // bs]), h, p % bs, e] = 0x7f + 0x80 * (
+                i & 1)
+            bad[b, h, e] = min(bad[b, h, e], p)
+    out, out16 = prefill(pkv, pool, q, start, 0.09, max(new))
+    pos = np.array(positions(ctx, new))
+    want = np.repeat(bad[pos[:, 0]] <= pos[:, 1][:, None, None], group,
+                     axis=1)
+    assert want.any() and not want.all()
+    got = to64(out)
+    np.testing.assert_array_equal(np.isnan(got), want)
+    assert torch.equal(torch.isnan(out16), torch.isnan(out))
+    np.testing.assert_array_equal(got[~want], to64(clean)[~want])
