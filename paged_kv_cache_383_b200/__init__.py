@@ -474,17 +474,26 @@ def _check_q8(k_cache, v_cache, k_scales, v_scales, names=("", "")):
     return shape
 
 
+# Turns over original_len between which a pair is partly scaled: each method's
+# published values.
+_ROPE_BANDS = {"wavelength": (1.0, 4.0), "yarn": (1.0, 32.0)}
+
+
 def pa_rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling=None,
                   factor: float = 1.0, original_len: int = 0,
-                  low: float = 1.0, high: float = 4.0):
+                  low: float | None = None, high: float | None = None):
     """(freqs, rope_scale) for ``pa_append``: the angular frequencies of the
     rot_dim/2 pairs as a float64 CPU tensor (move it to the device once) and
     the factor of cos and sin.  ``scaling``: None, "linear", "wavelength" or
-    "yarn" (``low`` / ``high``: turns over ``original_len``)."""
+    "yarn" (``low`` / ``high``: turns over ``original_len``, by default 1 and
+    4 for "wavelength", 1 and 32 for "yarn")."""
     import torch
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling {scaling!r} is none of "
                          f"{list(_ROPE_SCALINGS)}")
+    band = _ROPE_BANDS.get(scaling, (0.0, 0.0))
+    low = band[0] if low is None else low
+    high = band[1] if high is None else high
     d = _lib.pa_rope_desc(rot_dim=rot_dim, scaling=_ROPE_SCALINGS[scaling],
                           original_len=original_len, base=base, factor=factor,
                           low=low, high=high)

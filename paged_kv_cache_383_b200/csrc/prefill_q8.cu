@@ -725,10 +725,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || it.state == kEnd) break;
       // NaN codes that are taken out belong to the rows that see them: the
       // item's slot (flag, sequence, KV head, first key, row of position 0)
-      // tells the epilogue to look for them.  Its flag is cleared four items ahead: an item is
-      // published once every warp has taken up the one two before, so the
-      // slot's last readers (of eight items back) are done when it is cleared,
-      // and it is clear when its first writer comes.
+      // tells the epilogue to look for them.  Its flag is cleared four items
+      // ahead: an item is published once every warp has taken up the one two
+      // before, so the slot's last readers (of eight items back) are done when
+      // it is cleared, and it is clear when its first writer comes.
       int* nan_at = nan_s + kNanInts * (n % kNanSlots);
       if (ctid == 0) nan_s[kNanInts * ((n + 4) % kNanSlots)] = 0;
       if (it.state == kSkip) continue;

@@ -347,3 +347,18 @@ def test_16_bit_attention_takes_its_workspace_the_same_way(pkv, monkeypatch):
                        stream="side")
     assert [s for _, s in asked] == ["side", "side"]
     assert all(n > 0 for n, _ in asked)
+
+
+def test_rope_freqs_default_bands(pkv):
+    """Without low and high, each method's own: 1 and 32 turns for yarn, 1 and
+    4 by wavelength; one of them may be given alone."""
+    import torch
+    kw = dict(base=10000.0, factor=8.0, original_len=8192)
+    for scaling, high in (("yarn", 32.0), ("wavelength", 4.0)):
+        want, _ = pkv.pa_rope_freqs(128, scaling=scaling, low=1.0, high=high,
+                                    **kw)
+        for band in ({}, {"low": 1.0}, {"high": high}):
+            got, _ = pkv.pa_rope_freqs(128, scaling=scaling, **band, **kw)
+            assert torch.equal(got, want)
+        other, _ = pkv.pa_rope_freqs(128, scaling=scaling, high=2 * high, **kw)
+        assert not torch.equal(other, want)
