@@ -284,7 +284,8 @@ typedef struct {
   int num_blocks;
   pa_dtype dtype;
   int total_q;          /* rows of q and out */
-  int max_q_len;        /* host bound on any sequence's new-token count */
+  int max_q_len;        /* host bound on any sequence's new-token count (0:
+                           there are none, the call does nothing) */
   int max_context_len;  /* host bound on context_lens[] (0: table capacity) */
   int kernel;           /* pa_prefill_kernel (0: automatic) */
   int out_fp32;         /* as in pa_decode_desc: 1 = out is float32 */
@@ -437,7 +438,9 @@ typedef struct {
   int num_blocks;
   pa_dtype dtype;        /* of q, k, v, the norm weights and q_out */
   int total_q;           /* rows of q, k, v and q_out */
-  int max_q_len;         /* host bound on any sequence's new tokens */
+  int max_q_len;         /* host bound on any sequence's new tokens (0: there
+                            are none, the call does nothing); without
+                            query_start it does not matter */
   int rot_dim;           /* leading elements of a head that turn; 0: none */
   int rope_layout;       /* pa_rope_layout */
   float rope_scale;      /* factor of cos and sin (usually 1) */

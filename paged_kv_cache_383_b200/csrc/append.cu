@@ -675,7 +675,9 @@ pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
     return fail(PA_ERR_INVALID_ARG,
                 "%s: without query_start every sequence has one row, but "
                 "total_q %d != num_seqs %d", fn, d->total_q, d->num_seqs);
-  if (d->num_seqs == 0 || d->total_q == 0 || d->max_q_len == 0) return PA_OK;
+  // (one row per sequence needs no bound)
+  const int max_q_len = query_start ? d->max_q_len : 1;
+  if (d->num_seqs == 0 || d->total_q == 0 || max_q_len == 0) return PA_OK;
   if (!k_cache || !v_cache || !k || !v || !block_tables || !context_lens ||
       (d->num_q_heads > 0 && (!q || !q_out)) ||
       (kQ8 && (!k_scales || !v_scales)))
@@ -723,7 +725,7 @@ pa_status append(const char* fn, void* q_out, void* k_cache, void* v_cache,
   a.max_blocks_per_seq = d->max_blocks_per_seq;
   a.num_blocks = d->num_blocks;
   a.total_q = d->total_q;
-  a.max_q_len = d->max_q_len;
+  a.max_q_len = max_q_len;
   a.rot_pairs = d->rot_dim / 2;
   a.interleaved = d->rope_layout == PA_ROPE_INTERLEAVED;
   a.rope_scale = d->rope_scale;

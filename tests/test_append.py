@@ -362,3 +362,14 @@ def test_rope_freqs_default_bands(pkv):
             assert torch.equal(got, want)
         other, _ = pkv.pa_rope_freqs(128, scaling=scaling, high=2 * high, **kw)
         assert not torch.equal(other, want)
+
+
+@pytest.mark.parametrize("name", ["pa_append", "pa_append_q8"])
+def test_append_without_query_start_needs_no_bound(pkv, name):
+    """max_q_len 0 there is no call without rows: the checks behind that exit
+    (here the pool's) are reached."""
+    from paged_kv_cache_383_b200 import _lib
+    n = 12 if name == "pa_append" else 14
+    ptrs = [FAKE] * (n - 1) + [None]
+    assert _call(name, _append_desc(max_q_len=0, num_blocks=0), ptrs) == 1
+    assert b"empty block pool" in _lib.load().pa_last_error()

@@ -8,6 +8,8 @@ which stays below 2^-20 of the magnitudes that enter it: |u| + |w| of the
 rotated pair.  Then half a step of the type: eps / 2 of the value (16 bits),
 half the distance of e4m3 values (codes).
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -533,3 +535,32 @@ def test_offsets_past_4_gib(pkv):
         assert torch.equal(vc[blk].view(torch.uint8),
                            kc[blk].view(torch.uint8))
     assert int((ks != 0).sum()) == 2 * hkv
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("bound", [0, 1, 9])
+def test_without_query_start_the_bound_does_not_matter(pkv, q8, bound):
+    """Through the C ABI, which the binding gives a bound of 1."""
+    from paged_kv_cache_383_b200 import _lib
+    lib = _lib.load()
+    fn = lib.pa_append_q8 if q8 else lib.pa_append
+    n, hkv, d, bs = 5, 2, 64, 16
+    rows = torch.randn(n, hkv, d, device="cuda").half()
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[:, None]
+    table = table.contiguous()
+    lens = torch.ones(n, dtype=torch.int32, device="cuda")
+    pool = [torch.zeros(n, hkv, bs, d, device="cuda").to(
+        E4M3 if q8 else torch.float16) for _ in "kv"]
+    if q8:
+        pool += [torch.zeros(n, hkv, device="cuda") for _ in "kv"]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    desc = _lib.pa_append_desc(n, 0, hkv, d, bs, 1, n, _lib.PA_F16, n, bound,
+                               0, 0, 1.0, 1e-6, 0, hkv * d, hkv * d, 0)
+    st = fn(None, *[p.data_ptr() for p in pool], None, rows.data_ptr(),
+            rows.data_ptr(), None, None, None, table.data_ptr(),
+            lens.data_ptr(), None, ctypes.byref(desc), err.data_ptr(),
+            torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and err.item() == 0
+    for p in pool[:2]:
+        assert (p[:, :, 0].float() != 0).any(-1).all()
