@@ -137,3 +137,34 @@ def test_calls_on_two_streams_without_a_workspace(pkv, q8, handle):
             torch.cuda.synchronize()
             for i, out in enumerate(got):
                 assert torch.equal(out, want[kind][i % 2])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_append_on_a_stream_of_its_own(pkv, q8):
+    """The same bits as on the current stream."""
+    hq, hkv, d, bs, n = 8, 2, 64, 16, 30
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(n, hq + 2 * hkv, d, generator=g, device="cuda").half()
+    table = torch.randperm(n, generator=g, device="cuda").int()[:, None]
+    table = table.contiguous()
+    lens = torch.arange(n, device="cuda").int() % bs + 1
+    freqs = pkv.pa_rope_freqs(32)[0].cuda()
+    pool0 = [torch.randn(n, hkv, bs, d, generator=g, device="cuda").to(
+        E4M3 if q8 else torch.float16) for _ in "kv"]
+    if q8:
+        pool0 += [torch.full((n, hkv), 2.0 ** -8, device="cuda") for _ in "kv"]
+    fn = pkv.pa_append_q8 if q8 else pkv.pa_append
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (None, side, side.cuda_stream):
+        pool = [p.clone() for p in pool0]
+        q = torch.zeros(n, hq, d, device="cuda").half()
+        torch.cuda.synchronize()
+        fn(q, *pool, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], table,
+           lens, rope_freqs=freqs, rope_layout="interleaved", stream=stream)
+        torch.cuda.synchronize()
+        assert (q != 0).any(-1).all()
+        got.append([q] + [p.view(torch.uint8) for p in pool])
+    for a, b, c in zip(*got):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    assert not torch.equal(got[0][1], pool0[0].view(torch.uint8))

@@ -158,3 +158,34 @@ def test_nan_values_reach_the_rows_that_see_them(pkv, group, new, bs, d):
     np.testing.assert_array_equal(np.isnan(got), want)
     assert torch.equal(torch.isnan(out16), torch.isnan(out))
     np.testing.assert_array_equal(got[~want], to64(clean)[~want])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_v_scales_over_60_binades(pkv, dtype):
+    """Block by block, zeros among them, with large, tiny and zero queries and
+    peaked scores: within the documented 2^-33 of the largest scale, and the
+    16-bit output is the float32 one's rounding, infinities included."""
+    ctx, new = [300, 77], [5, 77]
+    pool = Pool(2, 128, 16, ctx, seed=8)
+    e = torch.arange(pool.n, device="cuda") * 37 % 61 - 30
+    ok = ~torch.isnan(pool.vs)
+    pool.vs.copy_(torch.where(
+        ok, torch.exp2(e.float())[:, None].expand(pool.n, 2), pool.vs))
+    for c, s, b in ((pool.vc, pool.vs, pool.table[0, 3]),
+                    (pool.vc, pool.vs, pool.table[1, 0]),
+                    (pool.kc, pool.ks, pool.table[0, 5])):
+        c[int(b)] = torch.zeros_like(c[int(b)].float()).to(E4M3)
+        s[int(b)] = 0.0
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn(82, 16, 128, generator=g, device="cuda")
+    q[:, 3] *= 50
+    q[:, 4] *= 2.0 ** -13
+    q[:, 5] = 0
+    q[:, 6, 7] = 300  # one large element among small ones
+    q = q.to(dtype)
+    for out, ref, tol in both(pkv, pool, q, [0, 5, 82], 0.05, 77):
+        # 300 / 50 times larger scores: arguments to 2^10, so 2^-13 on a
+        # weight, and as much on their sum
+        _, mag = reference(pool, q, positions(ctx, new), 0.05)
+        mag = mag[[4, 81]] if len(ref) == 2 else mag
+        assert (np.abs(to64(out) - ref) <= tol + 2.0 ** -12 * mag).all()
