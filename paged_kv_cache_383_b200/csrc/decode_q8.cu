@@ -15,8 +15,8 @@
 //    elements: ks joins the score's factor (once per page), vs joins the
 //    weight.
 //  * q is put into fp16 too, multiplied by the power of two that takes its
-//    largest element to [2^14, 2^15); that is exact for fp16 q and loses
-//    nothing above 2^-39 of the largest element for bf16 q.
+//    largest element to [2^14, 2^15): exact for elements above 2^-28 of the
+//    largest, and to 2^-39 of it for smaller ones.
 //  * K fragments: an 8x8 ldmatrix of 16-bit pairs gives a lane four
 //    consecutive codes of one row; the MMA's inner index may be any
 //    permutation of head_dim that both operands share, so the lane's codes
@@ -28,8 +28,11 @@
 //    E follows the exponent of the largest vs met so far (o is rescaled when
 //    it grows by more than 3), so w stays below 2^14 and small weights stay
 //    normal down to 2^-24.  The rounding is 2^-11 of a weight, an eighth of a
-//    bf16 output's own 2^-8.  With fp16 outputs it would show, so there the
-//    weight's residual is a second MMA operand, as in the 16-bit kernel.
+//    bf16 output's own 2^-8 (which hides it: against fp64 the bf16 outputs
+//    of 256 sequences are off by 1.6e-3 with and without; a float32 output of
+//    a bf16 call carries it).  With fp16 outputs it would show, so there the
+//    weight's residual is a second MMA operand, as in the 16-bit kernel; for
+//    bf16 it would take 197 us instead of 190 (batch 256 at 486k tokens).
 //
 // The split of the work, the ring of TMA pages (swizzled 128 bytes wide at
 // head_dim 128, 64 at 64), the bounded waits, the longest-first order and the
@@ -84,11 +87,14 @@ constexpr size_t smem_bytes_q8(int pages) {
 
 // CTAs per SM and the ring of one.  The consumers' work per byte is twice the
 // 16-bit cache's, so warps matter more than bytes in flight: blocks of 16 run
-// five CTAs of 32 KB (batch 256 at 486k tokens: 185 us with three of 64 KB,
-// 176 with four of 48, 172 with five of 32).  Blocks of 32 hold two slices of
-// scores and need the registers of three CTAs; with smaller rings or registers
-// they lose (434k tokens in 8 contexts: 143 us with three of 64 KB, 148 of 48,
-// 163 with registers for four).
+// five CTAs of 32 KB, whose 72 registers spill 132 to 148 bytes at head_dim
+// 128.  Blocks of 32 hold two slices of scores and need the registers of three
+// CTAs of 64 KB.  Measured, us, three CTAs of 64 KB / four of 48 / five of 32
+// (bf16; fp16 is the same to 3 %; 432k tokens in 256 contexts, and 481k in 8):
+//   blocks of 16, head_dim 128   196 / 177 / 173   224 / 204 / 220
+//   blocks of 16, head_dim 64    149 / 128 / 116   198 / 151 / 151
+//   blocks of 32, head_dim 128   159 / 169 / 175   191 / 188 / 216
+//   blocks of 32, head_dim 64    104 / 101 / 95    124 / 118 / 130
 constexpr int ctas_q8(int bs) { return bs == 16 ? 5 : 3; }
 constexpr int ring_bytes_q8(int bs) { return bs == 16 ? 32768 : 65536; }
 

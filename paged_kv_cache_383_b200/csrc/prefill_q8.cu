@@ -17,8 +17,8 @@
 //    their scales; the tile each query tile works on is converted once per
 //    128 query rows, next to 128 x 64 exponentials.
 //  * q is put into fp16 times the power of two that takes its row's largest
-//    element to [2^14, 2^15): exact for fp16, and for bf16 down to 2^-39 of
-//    the largest element.
+//    element to [2^14, 2^15): exact for elements above 2^-28 of the largest,
+//    and to 2^-39 of it for smaller ones.
 //  * ks is one factor per block of keys in the exponent's argument (a max per
 //    block, then one product).  vs joins the argument as log2(vs) - E: the
 //    exponential gives p vs / 2^E directly, and the row's sum of p is
