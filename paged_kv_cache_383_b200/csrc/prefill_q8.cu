@@ -42,7 +42,7 @@
 // and 14 issue the MMAs, whole warps with an elected thread (a lone thread
 // spends about 90 cycles on each).  Half of q's dims sit in tensor memory: at
 // 64 keys a tile, reading both operands of S from shared memory bounds it.
-// 8 chunks of 512 rows over 26k tokens with 64 query heads: 634 us, against
+// 8 chunks of 512 rows over 26k tokens with 64 query heads: 627 us, against
 // 767 with one query tile per CTA and two CTAs per SM, 721 with 128-key tiles.
 // A tile pair takes about 2600 cycles of an SM; its MMAs need 1450 and its
 // exponentials 1024, the rest is the latency between the steps.
@@ -72,7 +72,8 @@ constexpr int kScaleSlots = 16;  // tiles whose scales are staged
 constexpr int kConvWarp = 8, kPageWarp = 12, kMmaWarp = 13;
 constexpr int kThreads = 16 * 32;  // whole warpgroups; warp 15 has no work
 // Registers: 128 a thread at launch, shared out anew between the warpgroups
-// (a softmax thread holds 64 scores).  The sum must not exceed the launch's:
+// (a softmax thread holds 64 scores; converters that had 48 spilled, 645 us
+// instead of 627 for the chunks above).  The sum must not exceed the launch's:
 // an increase waits for registers that the others gave up.
 constexpr int kLaunchRegs = 128;
 constexpr int kSoftmaxRegs = 192, kConvRegs = 56, kIssueRegs = 72;
@@ -81,6 +82,8 @@ static_assert(2 * kSoftmaxRegs + kConvRegs + kIssueRegs == 4 * kLaunchRegs,
 // What the page warp stages for a tile: for each of its blocks ks, the
 // exponent log2(vs) - E + kShift and 2^-that; and E, last.
 constexpr int kSlotFloats = 16;
+// For each of eight items in turn, where NaN codes of V were taken out (see the
+// converters).
 constexpr int kNanSlots = 8, kNanInts = 8;
 // Tensor memory columns, for each query tile: S 64, P 32, the last 64 dims of
 // q 32, O head_dim (up to 128).

@@ -168,3 +168,47 @@ def test_append_on_a_stream_of_its_own(pkv, q8):
     for a, b, c in zip(*got):
         assert torch.equal(a, b) and torch.equal(a, c)
     assert not torch.equal(got[0][1], pool0[0].view(torch.uint8))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("handle", [False, True])
+def test_captured_on_a_stream_without_a_workspace(pkv, q8, handle):
+    """Attention captured on the stream it is given, its workspaces out of the
+    graph's memory: replays equal eager calls, also with eager calls between
+    that take their memory where the capture's was freed."""
+    hq, hkv, d, bs = 16, 4, 64, 16
+    torch.manual_seed(6)
+    table = torch.randperm(60).int().view(2, 30).cuda()
+    lens = torch.tensor([470, 33], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 9, 12], dtype=torch.int32, device="cuda")
+    pool = [torch.randn(60, hkv, bs, d, device="cuda").to(
+        E4M3 if q8 else torch.bfloat16) for _ in "kv"]
+    if q8:
+        pool += [torch.rand(60, hkv, device="cuda") + 0.5 for _ in "kv"]
+    q = torch.randn(12, hq, d, device="cuda").bfloat16()
+    decode = pkv.pa_decode_q8 if q8 else pkv.pa_decode
+    prefill = pkv.pa_prefill_q8 if q8 else pkv.pa_prefill
+
+    def step(a, b, stream=None):
+        decode(a, q[:2], *pool, table, lens, 0.125, partition_size=32,
+               stream=stream)
+        prefill(b, q, *pool, table, lens, start, 0.125, max_q_len=9,
+                stream=stream)
+
+    want, got = ([torch.zeros_like(q[:2]), torch.zeros_like(q)] for _ in "12")
+    step(*want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(*got, stream=side.cuda_stream if handle else side)
+    for _ in range(4):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        junk = [torch.full((1 << 16,), float("nan"), device="cuda")
+                for _ in range(4)]
+        step(*want)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
