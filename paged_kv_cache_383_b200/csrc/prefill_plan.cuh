@@ -230,6 +230,9 @@ pa_status check_prefill(const char* fn, const void* out, const void* q,
                 "%s: needs head_dim 64 or 128 (got %d), block_size "
                 "16 or 32 (got %d) and a query group of 1, 2, 4 or 8 (got %d)", fn,
                 d->head_dim, d->block_size, G);
+  if (static_cast<int64_t>(d->max_blocks_per_seq) * d->block_size >
+      0x7fffffffLL)
+    return fail(PA_ERR_INVALID_ARG, "%s: max_blocks_per_seq too large", fn);
   if (nothing_to_do(d)) return PA_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens ||
       !query_start)

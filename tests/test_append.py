@@ -373,3 +373,25 @@ def test_append_without_query_start_needs_no_bound(pkv, name):
     ptrs = [FAKE] * (n - 1) + [None]
     assert _call(name, _append_desc(max_q_len=0, num_blocks=0), ptrs) == 1
     assert b"empty block pool" in _lib.load().pa_last_error()
+
+
+@pytest.mark.parametrize("name", ["pa_prefill", "pa_prefill_q8"])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_prefill_refuses_a_table_past_2_31_tokens(pkv, name, bs):
+    """Its token count would not fit the kernels' 32-bit lengths; the largest
+    that does is let through (to the check of the workspace)."""
+    from paged_kv_cache_383_b200 import _lib
+    lib = _lib.load()
+
+    def call(blocks):
+        d = _lib.pa_prefill_desc(
+            num_seqs=2, num_q_heads=8, num_kv_heads=2, head_dim=128,
+            block_size=bs, max_blocks_per_seq=blocks, num_blocks=16, dtype=1,
+            total_q=10, max_q_len=8)
+        n = 7 if name == "pa_prefill" else 9
+        return getattr(lib, name)(*[FAKE] * n, 1.0, ctypes.byref(d), None, 0,
+                                  None, None)
+    assert call(2 ** 31 // bs) == 1
+    assert name.encode() + b": max_blocks_per_seq" in lib.pa_last_error()
+    assert call(2 ** 32 // bs + 4) == 1
+    assert call(2 ** 31 // bs - 1) == _lib.PA_ERR_WORKSPACE
