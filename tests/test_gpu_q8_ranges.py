@@ -189,3 +189,32 @@ def test_v_scales_over_60_binades(pkv, dtype):
         _, mag = reference(pool, q, positions(ctx, new), 0.05)
         mag = mag[[4, 81]] if len(ref) == 2 else mag
         assert (np.abs(to64(out) - ref) <= tol + 2.0 ** -12 * mag).all()
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_nan_values_among_many_items(pkv, few):
+    """Several dozen work items per CTA, NaN V codes in a few of the sequences:
+    where one is found is forgotten with its item."""
+    rng = np.random.default_rng(7)
+    n, hkv, d, bs = 900, 8, 64, 16
+    ctx = rng.integers(1, 90, n)
+    new = np.minimum(rng.integers(0, 5 if few else 90, n), ctx)
+    if few:   # a batch that shares keys between the query tiles
+        ctx[::50] += 400
+    pool = Pool(hkv, d, bs, ctx.tolist(), seed=12)
+    start = np.concatenate([[0], np.cumsum(new)])
+    q = torch.randn(int(start[-1]), hkv, d, device="cuda").to(BF)
+    clean, _ = prefill(pkv, pool, q, start, 0.125, int(new.max()))
+    bad = np.full((n, hkv, d), 1 << 30)
+    raw = pool.vc.view(torch.uint8)
+    for b in rng.choice(n, 90, replace=False):
+        p, h, e = (int(rng.integers(0, m)) for m in (ctx[b], hkv, d))
+        raw[int(pool.table[b, p // bs]), h, p % bs, e] = 0xff
+        bad[b, h, e] = p
+    out, _ = prefill(pkv, pool, q, start, 0.125, int(new.max()))
+    pos = np.array(positions(ctx.tolist(), new.tolist()))
+    want = bad[pos[:, 0]] <= pos[:, 1][:, None, None]
+    assert want.any()
+    got = to64(out)
+    np.testing.assert_array_equal(np.isnan(got), want)
+    np.testing.assert_array_equal(got[~want], to64(clean)[~want])
